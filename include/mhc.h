@@ -375,6 +375,115 @@ MHC_API int mhc_head(const uint16_t* R, const float* hc_fn, const float* hc_scal
                      size_t workspace_bytes, int64_t T, int64_t H, float norm_eps, float hc_eps,
                      mhc_stream_t stream);
 
+/*
+ * The answer end of the stack: what follows a pre-map's y or a head's row, for training and serving.
+ * No entry of these is on the pages; they are additions of this library. Rows lie `stride` elements
+ * apart (stride >= the row's length, so a slice of wider rows or a padded vocabulary is taken as it
+ * is), at any alignment of the element. Three element types:
+ */
+enum mhc_dtype {
+    MHC_DTYPE_BF16 = 0,
+    MHC_DTYPE_F16 = 1,
+    MHC_DTYPE_F32 = 2,
+};
+
+/*
+ * mhc_layer_norm  y = (x - mean) * rstd * gamma + beta over rows of H, mean = sum(x) / H,
+ *     rstd = 1 / sqrt(sum((x - mean)^2) / H + eps).
+ *   x     [T][H] of dtype, rows x_stride apart
+ *   gamma, beta [H] of w_dtype (MHC_DTYPE_F32 or dtype); NULL: ones / zeros
+ *   y     [T][H] of dtype, dense, rounded once from fp32; may be exactly x where x_stride == H
+ *   mean, rstd [T] fp32 out, or NULL; what the backward pass takes
+ *   1 <= H <= 2^28 (as V below); eps > 0.
+ *
+ * mhc_layer_norm_backward  with xh = (x - mean) * rstd and q = d_y * gamma:
+ *     d_x = rstd * (q - sum(q)/H - xh * sum(q * xh)/H)   [T][H] of dtype, dense
+ *     d_gamma = sum_t d_y * xh, d_beta = sum_t d_y       [H] fp32, each may be NULL; token sums
+ *   are in a fixed order. x, gamma, mean, rstd as the forward pass took and gave them. With T == 0
+ *   d_gamma and d_beta are set to zero (the one thing written); workspace of
+ *   mhc_layer_norm_backward_workspace_bytes(T, H) bytes, 256-byte aligned.
+ * Errors: MHC_ERR_INVALID_ARG, MHC_ERR_WORKSPACE_TOO_SMALL, MHC_ERR_ALIAS (an output overlapping an
+ * input or another output, y == x apart).
+ */
+MHC_API int mhc_layer_norm(const void* x, int64_t x_stride, int dtype, const void* gamma,
+                           const void* beta, int w_dtype, void* y, float* mean, float* rstd,
+                           int64_t T, int64_t H, float eps, mhc_stream_t stream);
+MHC_API size_t mhc_layer_norm_backward_workspace_bytes(int64_t T, int64_t H);
+MHC_API int mhc_layer_norm_backward(const void* d_y, int64_t dy_stride, const void* x,
+                                    int64_t x_stride, int dtype, const void* gamma, int w_dtype,
+                                    const float* mean, const float* rstd, void* d_x, float* d_gamma,
+                                    float* d_beta, void* workspace, size_t workspace_bytes,
+                                    int64_t T, int64_t H, mhc_stream_t stream);
+
+/* Limits of the two operators below. */
+enum {
+    MHC_TOP_MAX = 32,        /* top alternatives of mhc_token_logprobs */
+    MHC_DISTILL_MAX = 1024,  /* teacher entries per row of mhc_distill_topk */
+};
+
+/*
+ * mhc_token_logprobs  of the distribution p = softmax(logits / temperature) of each row:
+ *   logits  [T][V] of dtype, rows row_stride apart
+ *   targets [T] int64, or NULL (then logprob is NULL too). A negative target means "none" (padding):
+ *           its log probability is 0. A target >= V gives NaN.
+ *   logprob [T] fp32 out: ln p[target]
+ *   entropy [T] fp32 out, or NULL: -sum_v p_v ln p_v (0 ln 0 = 0)
+ *   top, top_index [T][top] int64 out, top_logprob [T][top] fp32 out: the `top` largest logits in
+ *           falling order (0 <= top <= min(V, MHC_TOP_MAX)), equal ones by the lower index, and
+ *           their log probabilities
+ *   stats   [T][2] fp32 out, or NULL: the row's largest logit m and
+ *           s = sum_v exp((logits_v - m) / temperature); what the backward pass takes
+ * -infinity masks a logit; the lowest finite value is a value. A row of -infinity alone has no
+ * distribution: s = 0, entropy 0, log probabilities -infinity, no gradient. A row with a NaN or a
+ * +infinity gives NaN everywhere and top indices of -1.
+ *
+ * mhc_token_logprobs_backward  d_logits = (d_logprob (1[v = target] - p_v)
+ *                                          - d_entropy p_v (ln p_v + entropy)) / temperature
+ *   d_logprob, d_entropy [T] fp32, one of them may be NULL (zero); entropy as the forward pass gave
+ *   it (with d_entropy); targets with d_logprob. d_logits [T][V] of dtype, rows d_row_stride apart,
+ *   rounded once; may be exactly logits (same stride). Rows whose upstream gradients are zero get
+ *   zeros, whatever their logits. The top alternatives have no gradient.
+ * temperature: finite and > 0 (and so are 1 / temperature and log2(e) / temperature).
+ * Errors: MHC_ERR_INVALID_ARG; MHC_ERR_ALIAS (an output overlapping an input, in place apart).
+ */
+MHC_API int mhc_token_logprobs(const void* logits, int64_t row_stride, int dtype,
+                               const int64_t* targets, float temperature, float* logprob,
+                               float* entropy, int top, int64_t* top_index, float* top_logprob,
+                               float* stats, int64_t T, int64_t V, mhc_stream_t stream);
+MHC_API int mhc_token_logprobs_backward(const void* logits, int64_t row_stride, int dtype,
+                                        const int64_t* targets, float temperature,
+                                        const float* stats, const float* d_logprob,
+                                        const float* d_entropy, const float* entropy,
+                                        void* d_logits, int64_t d_row_stride, int64_t T, int64_t V,
+                                        mhc_stream_t stream);
+
+/*
+ * mhc_distill_topk  distillation from a teacher's K kept logits per row:
+ *     w = softmax over the row's used entries of teacher / temperature,
+ *     p = softmax over all of logits / temperature,
+ *     loss = sum_k w_k (ln w_k - ln p[index_k]).
+ *   index   [T][K] int64: token of each entry; negative: an unused entry (rows may keep fewer than
+ *           K). An index >= V makes the row NaN. An index given twice counts twice.
+ *   teacher [T][K] of teacher_dtype: logits (or log probabilities: the shift cancels)
+ *   loss [T], weights [T][K] (w, 0 in unused entries), stats [T][2] (as mhc_token_logprobs): fp32
+ *           out. A row without a used entry (or whose teacher logits are all -infinity) has loss 0.
+ *   1 <= K <= MHC_DISTILL_MAX.
+ *
+ * mhc_distill_topk_backward  d_logits = d_loss (p_v - sum_{k: index_k = v} w_k) / temperature
+ *   (zero in rows without a used entry and where d_loss is 0), from the forward pass's weights and
+ *   stats; d_loss [T] fp32; d_logits as in mhc_token_logprobs_backward.
+ * Errors as above.
+ */
+MHC_API int mhc_distill_topk(const void* logits, int64_t row_stride, int dtype,
+                             const int64_t* index, const void* teacher, int teacher_dtype,
+                             float temperature, float* loss, float* weights, float* stats,
+                             int64_t T, int64_t V, int64_t K, mhc_stream_t stream);
+MHC_API int mhc_distill_topk_backward(const void* logits, int64_t row_stride, int dtype,
+                                      const int64_t* index, const float* weights,
+                                      const float* stats, const float* d_loss, float temperature,
+                                      void* d_logits, int64_t d_row_stride, int64_t T, int64_t V,
+                                      int64_t K, mhc_stream_t stream);
+
 /* Number of kernel launches this process has enqueued through the library so far (all devices,
  * all threads). A diagnostic counter for benchmarks: take the difference around a region. */
 MHC_API uint64_t mhc_launch_count(void);

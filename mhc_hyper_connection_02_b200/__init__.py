@@ -38,6 +38,12 @@ POST_PATH_VEC8 = 11
 POST_PATH_PERSISTENT = 12
 POST_PATH_SCALAR = 13
 
+DTYPE_BF16 = 0
+DTYPE_F16 = 1
+DTYPE_F32 = 2
+TOP_MAX = 32
+DISTILL_MAX = 1024
+
 EXPORTED_SYMBOLS = (
     "mhc_default_params", "mhc_pre", "mhc_pre_workspace_bytes", "mhc_post", "mhc_sinkhorn",
     "mhc_pre_with_path", "mhc_post_with_path", "mhc_device_status", "mhc_status_string",
@@ -45,7 +51,9 @@ EXPORTED_SYMBOLS = (
     "mhc_pre_big_fuse_with_prenorm", "mhc_expand", "mhc_head_mean", "mhc_head",
     "mhc_head_workspace_bytes", "mhc_post_project", "mhc_post_project_splits",
     "mhc_post_project_workspace_bytes", "mhc_post_backward", "mhc_pre_backward",
-    "mhc_pre_backward_workspace_bytes", "mhc_selftest_wait_timeout",
+    "mhc_pre_backward_workspace_bytes", "mhc_selftest_wait_timeout", "mhc_layer_norm",
+    "mhc_layer_norm_backward", "mhc_layer_norm_backward_workspace_bytes", "mhc_token_logprobs",
+    "mhc_token_logprobs_backward", "mhc_distill_topk", "mhc_distill_topk_backward",
 )
 
 
@@ -132,6 +140,26 @@ def lib() -> ctypes.CDLL:
     L.mhc_pre_backward.restype = ctypes.c_int
     L.mhc_pre_backward.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                    ctypes.c_size_t, _I64, _I64, ctypes.POINTER(Params), _P]
+    L.mhc_layer_norm.restype = ctypes.c_int
+    L.mhc_layer_norm.argtypes = [_P, _I64, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _I64,
+                                 _I64, ctypes.c_float, _P]
+    L.mhc_layer_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.mhc_layer_norm_backward_workspace_bytes.argtypes = [_I64, _I64]
+    L.mhc_layer_norm_backward.restype = ctypes.c_int
+    L.mhc_layer_norm_backward.argtypes = [_P, _I64, _P, _I64, ctypes.c_int, _P, ctypes.c_int, _P,
+                                          _P, _P, _P, _P, _P, ctypes.c_size_t, _I64, _I64, _P]
+    L.mhc_token_logprobs.restype = ctypes.c_int
+    L.mhc_token_logprobs.argtypes = [_P, _I64, ctypes.c_int, _P, ctypes.c_float, _P, _P,
+                                     ctypes.c_int, _P, _P, _P, _I64, _I64, _P]
+    L.mhc_token_logprobs_backward.restype = ctypes.c_int
+    L.mhc_token_logprobs_backward.argtypes = [_P, _I64, ctypes.c_int, _P, ctypes.c_float, _P, _P,
+                                              _P, _P, _P, _I64, _I64, _I64, _P]
+    L.mhc_distill_topk.restype = ctypes.c_int
+    L.mhc_distill_topk.argtypes = [_P, _I64, ctypes.c_int, _P, _P, ctypes.c_int, ctypes.c_float,
+                                   _P, _P, _P, _I64, _I64, _I64, _P]
+    L.mhc_distill_topk_backward.restype = ctypes.c_int
+    L.mhc_distill_topk_backward.argtypes = [_P, _I64, ctypes.c_int, _P, _P, _P, _P,
+                                            ctypes.c_float, _P, _I64, _I64, _I64, _I64, _P]
     L.mhc_launch_count.restype = ctypes.c_uint64
     L.mhc_launch_count.argtypes = []
     _lib = L
@@ -480,6 +508,260 @@ def sinkhorn(logits, *, comb=None, iters: int = 20, eps: float = 1e-6, stream=No
                             _stream(stream))
     _check(st, "mhc_sinkhorn")
     return comb
+
+
+def _dtype(t, name):
+    import torch
+    code = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in code:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32 (got {t.dtype})")
+    return code[t.dtype]
+
+
+def _rows(t, name, shape=None, dtype=None, device=None):
+    """Checks a [T, N] CUDA tensor whose rows are dense and any distance apart; returns that
+    distance in elements."""
+    _dtype(t, name)
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor of two dimensions")
+    T, N = t.shape
+    if N < 1:
+        raise ValueError(f"{name} must have at least one column")
+    stride = t.stride(0) if T > 1 else N
+    if (N > 1 and t.stride(1) != 1) or stride < N:
+        raise ValueError(f"{name}: the elements of a row must be contiguous and rows must not "
+                         f"overlap (strides {tuple(t.stride())})")
+    if shape is not None and (T, N) != tuple(shape):
+        raise ValueError(f"{name} shape {(T, N)} != {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return stride
+
+
+class _Launch:
+    """The stream of a call on `device`: the given one (a torch stream or a handle), else the
+    device's current one. While it is entered, allocations belong to that stream; at the end the
+    tensors of the call are marked as used there, so that memory freed on their own stream is not
+    handed out again too early."""
+
+    def __init__(self, stream, device, *tensors):
+        import torch
+        current = torch.cuda.current_stream(device)
+        if stream is None:
+            stream = current
+        elif not isinstance(stream, torch.cuda.Stream):
+            stream = current if int(stream) == current.cuda_stream else \
+                torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        self.handle = ctypes.c_void_p(int(stream.cuda_stream))
+        self._other = stream if stream.cuda_stream != current.cuda_stream else None
+        self._tensors = tensors
+        self._scope = torch.cuda.stream(stream) if self._other is not None else None
+
+    def __enter__(self):
+        if self._scope is not None:
+            self._scope.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._scope is not None:
+            for t in self._tensors:
+                if t is not None:
+                    t.record_stream(self._other)
+            self._scope.__exit__(*exc)
+        return False
+
+
+def _need_on(t, dtype, shape, name, device):
+    _need(t, dtype, shape, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _norm_weight(t, name, x):
+    import torch
+    if t is None:
+        return None
+    code = _dtype(t, name)
+    if t.dtype not in (torch.float32, x.dtype):
+        raise ValueError(f"{name} must be float32 or of the rows' type {x.dtype} (got {t.dtype})")
+    _need_on(t, t.dtype, (x.shape[1],), name, x.device)
+    return code
+
+
+def layer_norm(x, gamma=None, beta=None, *, eps: float = 1e-6, y=None, mean=None, rstd=None,
+               stream=None):
+    """Layer norm of the rows of x [T,H] (bfloat16, float16 or float32; dense rows any distance
+    apart, such as one stream R[:, i] of a residual). gamma, beta [H] in float32 or x's type, or
+    None. Returns (y [T,H] of x's type, mean [T], rstd [T] fp32); pass y=x to norm in place."""
+    import torch
+    stride = _rows(x, "x")
+    T, H = x.shape
+    dev = x.device
+    wd = _norm_weight(gamma, "gamma", x)
+    bd = _norm_weight(beta, "beta", x)
+    if wd is not None and bd is not None and wd != bd:
+        raise ValueError("gamma and beta must be of one type")
+    with _Launch(stream, dev, x, gamma, beta, y, mean, rstd) as on:
+        y = torch.empty((T, H), dtype=x.dtype, device=dev) if y is None else y
+        mean = torch.empty(T, dtype=torch.float32, device=dev) if mean is None else mean
+        rstd = torch.empty(T, dtype=torch.float32, device=dev) if rstd is None else rstd
+        _need_on(y, x.dtype, (T, H), "y", dev)
+        _need_on(mean, torch.float32, (T,), "mean", dev)
+        _need_on(rstd, torch.float32, (T,), "rstd", dev)
+        st = lib().mhc_layer_norm(_ptr(x), stride, _dtype(x, "x"), _ptr(gamma), _ptr(beta),
+                                  wd if wd is not None else bd if bd is not None else DTYPE_F32,
+                                  _ptr(y), _ptr(mean), _ptr(rstd), T, H, float(eps), on.handle)
+    _check(st, "mhc_layer_norm")
+    return y, mean, rstd
+
+
+def layer_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    return int(lib().mhc_layer_norm_backward_workspace_bytes(int(T), int(H)))
+
+
+def layer_norm_backward(d_y, x, gamma, mean, rstd, *, d_x=None, workspace=None, stream=None):
+    """Backward of layer_norm from d_y [T,H] and the forward's x, gamma (or None), mean and rstd.
+    Returns (d_x [T,H] of x's type, d_gamma [H], d_beta [H] fp32)."""
+    import torch
+    xs = _rows(x, "x")
+    T, H = x.shape
+    dev = x.device
+    ds = _rows(d_y, "d_y", (T, H), x.dtype, dev)
+    wd = _norm_weight(gamma, "gamma", x)
+    _need_on(mean, torch.float32, (T,), "mean", dev)
+    _need_on(rstd, torch.float32, (T,), "rstd", dev)
+    with _Launch(stream, dev, d_y, x, gamma, mean, rstd, d_x, workspace) as on:
+        d_x = torch.empty((T, H), dtype=x.dtype, device=dev) if d_x is None else d_x
+        _need_on(d_x, x.dtype, (T, H), "d_x", dev)
+        d_gamma = torch.empty(H, dtype=torch.float32, device=dev)
+        d_beta = torch.empty(H, dtype=torch.float32, device=dev)
+        nws = layer_norm_backward_workspace_bytes(T, H)
+        if workspace is None and nws > 0:
+            workspace = torch.empty(nws, dtype=torch.uint8, device=dev)
+        if workspace is not None:
+            _need_on(workspace, workspace.dtype, None, "workspace", dev)
+        wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = lib().mhc_layer_norm_backward(
+            _ptr(d_y), ds, _ptr(x), xs, _dtype(x, "x"), _ptr(gamma),
+            DTYPE_F32 if wd is None else wd, _ptr(mean), _ptr(rstd), _ptr(d_x), _ptr(d_gamma),
+            _ptr(d_beta), _ptr(workspace), wsb, T, H, on.handle)
+    _check(st, "mhc_layer_norm_backward")
+    return d_x, d_gamma, d_beta
+
+
+def token_logprobs(logits, targets=None, *, temperature: float = 1.0, top: int = 0,
+                   entropy: bool = True, stream=None):
+    """Log probabilities of given tokens under softmax(logits / temperature). logits [T,V]
+    (bfloat16, float16 or float32; dense rows any distance apart), targets [T] int64 (negative:
+    none) or None. Returns (logprob [T] or None, entropy [T] or None, top_index [T,top] int64 and
+    top_logprob [T,top] or None when top is 0, stats [T,2] for the backward pass), fp32."""
+    import torch
+    stride = _rows(logits, "logits")
+    T, V = logits.shape
+    dev = logits.device
+    top = int(top)
+    if not 0 <= top <= min(V, TOP_MAX):
+        raise ValueError(f"top must be 0 to min(V, {TOP_MAX})")
+    if targets is not None:
+        _need_on(targets, torch.int64, (T,), "targets", dev)
+    with _Launch(stream, dev, logits, targets) as on:
+        f32 = dict(dtype=torch.float32, device=dev)
+        lp = torch.empty(T, **f32) if targets is not None else None
+        ent = torch.empty(T, **f32) if entropy else None
+        ti = torch.empty((T, top), dtype=torch.int64, device=dev) if top else None
+        tl = torch.empty((T, top), **f32) if top else None
+        stats = torch.empty((T, 2), **f32)
+        st = lib().mhc_token_logprobs(_ptr(logits), stride, _dtype(logits, "logits"),
+                                      _ptr(targets), float(temperature), _ptr(lp), _ptr(ent), top,
+                                      _ptr(ti), _ptr(tl), _ptr(stats), T, V, on.handle)
+    _check(st, "mhc_token_logprobs")
+    return lp, ent, ti, tl, stats
+
+
+def token_logprobs_backward(logits, targets, stats, d_logprob=None, *, d_entropy=None,
+                            entropy=None, temperature: float = 1.0, d_logits=None, stream=None):
+    """Gradient of token_logprobs' log probabilities and entropy to the logits, from the upstream
+    gradients d_logprob [T] and d_entropy [T] (either may be None; entropy [T] goes with
+    d_entropy) and the forward's stats. Returns d_logits [T,V] of the logits' type (pass
+    d_logits=logits to write it over them)."""
+    import torch
+    stride = _rows(logits, "logits")
+    T, V = logits.shape
+    dev = logits.device
+    if targets is not None:
+        _need_on(targets, torch.int64, (T,), "targets", dev)
+    _need_on(stats, torch.float32, (T, 2), "stats", dev)
+    for name, t in (("d_logprob", d_logprob), ("d_entropy", d_entropy), ("entropy", entropy)):
+        if t is not None:
+            _need_on(t, torch.float32, (T,), name, dev)
+    with _Launch(stream, dev, logits, targets, stats, d_logprob, d_entropy, entropy,
+                 d_logits) as on:
+        d_logits = torch.empty((T, V), dtype=logits.dtype, device=dev) if d_logits is None \
+            else d_logits
+        ds = _rows(d_logits, "d_logits", (T, V), logits.dtype, dev)
+        st = lib().mhc_token_logprobs_backward(
+            _ptr(logits), stride, _dtype(logits, "logits"), _ptr(targets), float(temperature),
+            _ptr(stats), _ptr(d_logprob), _ptr(d_entropy), _ptr(entropy), _ptr(d_logits), ds, T, V,
+            on.handle)
+    _check(st, "mhc_token_logprobs_backward")
+    return d_logits
+
+
+def distill_topk(logits, index, teacher, *, temperature: float = 1.0, stream=None):
+    """Distillation loss of logits [T,V] against a teacher's kept logits teacher [T,K] of the
+    tokens index [T,K] int64 (negative: unused). Returns (loss [T], weights [T,K], stats [T,2])
+    fp32; the last two go to distill_topk_backward."""
+    import torch
+    stride = _rows(logits, "logits")
+    T, V = logits.shape
+    dev = logits.device
+    _need_on(index, torch.int64, None, "index", dev)
+    if index.dim() != 2 or index.shape[0] != T or not 1 <= index.shape[1] <= DISTILL_MAX:
+        raise ValueError(f"index must be [T, K] with 1 <= K <= {DISTILL_MAX}")
+    K = index.shape[1]
+    td = _dtype(teacher, "teacher")
+    _need_on(teacher, teacher.dtype, (T, K), "teacher", dev)
+    with _Launch(stream, dev, logits, index, teacher) as on:
+        f32 = dict(dtype=torch.float32, device=dev)
+        loss, weights = torch.empty(T, **f32), torch.empty((T, K), **f32)
+        stats = torch.empty((T, 2), **f32)
+        st = lib().mhc_distill_topk(_ptr(logits), stride, _dtype(logits, "logits"), _ptr(index),
+                                    _ptr(teacher), td, float(temperature), _ptr(loss),
+                                    _ptr(weights), _ptr(stats), T, V, K, on.handle)
+    _check(st, "mhc_distill_topk")
+    return loss, weights, stats
+
+
+def distill_topk_backward(logits, index, weights, stats, d_loss, *, temperature: float = 1.0,
+                          d_logits=None, stream=None):
+    """Gradient of distill_topk's loss to the logits, from d_loss [T] and the forward's weights and
+    stats. Returns d_logits [T,V] of the logits' type (pass d_logits=logits to write over them)."""
+    import torch
+    stride = _rows(logits, "logits")
+    T, V = logits.shape
+    dev = logits.device
+    _need_on(index, torch.int64, None, "index", dev)
+    if index.dim() != 2 or index.shape[0] != T or not 1 <= index.shape[1] <= DISTILL_MAX:
+        raise ValueError(f"index must be [T, K] with 1 <= K <= {DISTILL_MAX}")
+    K = index.shape[1]
+    _need_on(weights, torch.float32, (T, K), "weights", dev)
+    _need_on(stats, torch.float32, (T, 2), "stats", dev)
+    _need_on(d_loss, torch.float32, (T,), "d_loss", dev)
+    with _Launch(stream, dev, logits, index, weights, stats, d_loss, d_logits) as on:
+        d_logits = torch.empty((T, V), dtype=logits.dtype, device=dev) if d_logits is None \
+            else d_logits
+        ds = _rows(d_logits, "d_logits", (T, V), logits.dtype, dev)
+        st = lib().mhc_distill_topk_backward(
+            _ptr(logits), stride, _dtype(logits, "logits"), _ptr(index), _ptr(weights),
+            _ptr(stats), _ptr(d_loss), float(temperature), _ptr(d_logits), ds, T, V, K, on.handle)
+    _check(st, "mhc_distill_topk_backward")
+    return d_logits
 
 
 def device_status(stream=None) -> int:

@@ -14,3 +14,5 @@
 #include "mhc_post_project.cu"
 #include "mhc_backward.cu"
 #include "mhc_backward_tc.cu"
+#include "mhc_norm.cu"
+#include "mhc_logits.cu"

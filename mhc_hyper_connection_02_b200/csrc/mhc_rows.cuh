@@ -1,0 +1,192 @@
+// Device-side helpers of the row operators (layer norm, token log probabilities, distillation):
+// element types, 16-byte windows over rows of any alignment, and block reductions in a fixed order.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "mhc_device.cuh"
+
+namespace mhc {
+
+// Element types (the values of enum mhc_dtype). kVec elements fill 16 bytes.
+template <int DT>
+struct Elem;
+
+template <>
+struct Elem<0> {  // bf16
+  using raw = uint16_t;
+  static constexpr int kVec = 8;
+  static constexpr int kOrderBits = 16;  // leading bits of order_key that tell values apart
+  static constexpr raw kNegInf = 0xff80;
+  static __device__ __forceinline__ float to_f32(raw v) { return bf16_to_f32(v); }
+  static __device__ __forceinline__ raw from_f32(float v) { return f32_to_bf16(v); }
+  static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      x[2 * q] = bf16_lo((&w.x)[q]);
+      x[2 * q + 1] = bf16_hi((&w.x)[q]);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
+  }
+};
+
+template <>
+struct Elem<1> {  // fp16
+  using raw = uint16_t;
+  static constexpr int kVec = 8;
+  static constexpr int kOrderBits = 19;
+  static constexpr raw kNegInf = 0xfc00;
+  static __device__ __forceinline__ float to_f32(raw v) {
+    return __half2float(__ushort_as_half(v));
+  }
+  static __device__ __forceinline__ raw from_f32(float v) {
+    return __half_as_ushort(__float2half_rn(v));
+  }
+  static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[8]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&(&w.x)[q]));
+      x[2 * q] = f.x;
+      x[2 * q + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+    uint4 w;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const __half2 h = __floats2half2_rn(x[2 * q], x[2 * q + 1]);
+      (&w.x)[q] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return w;
+  }
+};
+
+template <>
+struct Elem<2> {  // fp32
+  using raw = float;
+  static constexpr int kVec = 4;
+  static constexpr int kOrderBits = 32;
+  static __device__ __forceinline__ float to_f32(raw v) { return v; }
+  static __device__ __forceinline__ raw from_f32(float v) { return v; }
+  static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[4]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = __uint_as_float((&w.x)[q]);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                      __float_as_uint(x[3]));
+  }
+};
+
+// ------------------------------------------------------------------------------ windows
+//
+// A row of n elements at any element-aligned address is cut at the 16-byte boundaries of its
+// addresses: window s holds elements s * kVec - off .. + kVec, where `off` elements of window 0
+// (and the end of the last window) lie outside the row. Whole windows are read and written with
+// one 16-byte access, the first and the last by single elements where the row does not fill them,
+// so nothing outside the row is touched.
+
+template <int DT>
+__device__ __forceinline__ int window_offset(const void* row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) /
+                          sizeof(typename Elem<DT>::raw));
+}
+template <int DT>
+__device__ __forceinline__ int window_count(int off, int n) {
+  return (off + n + Elem<DT>::kVec - 1) / Elem<DT>::kVec;
+}
+
+// First element of window s (negative in a partial window 0).
+template <int DT>
+__device__ __forceinline__ int window_first(int s, int off) {
+  return s * Elem<DT>::kVec - off;
+}
+
+// Window s; what lies outside the row (all of it past the last window) comes back as -infinity.
+template <int DT>
+__device__ __forceinline__ uint4 load_window(const typename Elem<DT>::raw* row, int n, int off,
+                                             int s) {
+  using E = Elem<DT>;
+  const int e0 = window_first<DT>(s, off);
+  if (e0 >= 0 && e0 <= n - E::kVec) return ld_stream_ro(row + e0);
+  uint4 w;
+  if constexpr (DT == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = e0 + j;
+      (&w.x)[j] = (e >= 0 && e < n) ? __float_as_uint(row[e]) : 0xff800000u;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = e0 + 2 * j;
+      const uint32_t lo = (e >= 0 && e < n) ? row[e] : E::kNegInf;
+      const uint32_t hi = (e + 1 >= 0 && e + 1 < n) ? row[e + 1] : E::kNegInf;
+      (&w.x)[j] = lo | (hi << 16);
+    }
+  }
+  return w;
+}
+
+// ------------------------------------------------------------------------------ reductions
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Block reductions of NT threads: an xor tree in each warp, then the warps in order, the same bits
+// in every thread. `red` holds NT / 32 floats (2 NT / 32 for the pair); the leading barrier makes
+// it safe to use one array for several reductions.
+template <int NT>
+__device__ __forceinline__ float block_max(float v, float* red) {
+  v = warp_max(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int w = 1; w < NT / 32; ++w) v = fmaxf(v, red[w]);
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int w = 1; w < NT / 32; ++w) v += red[w];
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ float2 block_sum2(float a, float b, float* red) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    red[2 * (threadIdx.x >> 5)] = a;
+    red[2 * (threadIdx.x >> 5) + 1] = b;
+  }
+  __syncthreads();
+  a = red[0];
+  b = red[1];
+#pragma unroll
+  for (int w = 1; w < NT / 32; ++w) {
+    a += red[2 * w];
+    b += red[2 * w + 1];
+  }
+  return make_float2(a, b);
+}
+
+}  // namespace mhc
