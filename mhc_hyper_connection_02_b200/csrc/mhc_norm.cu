@@ -14,6 +14,8 @@
 // partial rows in order.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "mhc.h"
 #include "mhc_internal.h"
 #include "mhc_rows.cuh"
@@ -47,6 +49,397 @@ struct NormBwdArgs {
   int64_t T;
   int H;
 };
+
+// ------------------------------------------------------------------------------ rows in registers
+//
+// A group of G threads holds a row: thread i of it the accesses i, i + G, ..., N of them, of VW
+// elements each (16 bytes, or one element where the row's width, stride or address does not allow
+// more). The row is read once; mean, variance and output come from the registers.
+
+// Access of VW elements: 16 bytes kept packed until used, or one element.
+template <int DT, int VW>
+struct Chunk {
+  using E = Elem<DT>;
+  using raw = typename E::raw;
+  typename std::conditional<VW == 1, raw, uint4>::type v;
+  // kRo: not written by this kernel (read-only path). kKeep: worth keeping in L1 (weights).
+  __device__ __forceinline__ void load(const raw* p) {
+    if constexpr (VW == 1) v = *p; else v = ld_stream(p);
+  }
+  __device__ __forceinline__ void load_ro(const raw* p) {
+    if constexpr (VW == 1) v = __ldg(p); else v = ld_stream_ro(p);
+  }
+  __device__ __forceinline__ void get(float (&x)[VW]) const {
+    if constexpr (VW == 1) x[0] = E::to_f32(v); else E::unpack(v, x);
+  }
+  static __device__ __forceinline__ void put(raw* p, const float (&x)[VW]) {
+    if constexpr (VW == 1) *p = E::from_f32(x[0]); else st_stream(p, E::pack(x));
+  }
+};
+
+// VW weights at p (of the rows' type or fp32), through L1.
+template <int WT, int VW>
+__device__ __forceinline__ void load_weights(const typename Elem<WT>::raw* p, float (&g)[VW]) {
+  using W = Elem<WT>;
+  if constexpr (VW == 1) {
+    g[0] = W::to_f32(__ldg(p));
+  } else {
+#pragma unroll
+    for (int q = 0; q < VW; q += W::kVec) {
+      float x[W::kVec];
+      W::unpack(__ldg(reinterpret_cast<const uint4*>(p + q)), x);
+#pragma unroll
+      for (int k = 0; k < W::kVec; ++k) g[q + k] = x[k];
+    }
+  }
+}
+
+constexpr int kNormWarpRows = 4;  // rows per CTA of the one-warp-per-row forward form
+
+// Forward. kWarp: a warp per row, no barrier; otherwise the CTA holds one row (blockDim.x = G).
+template <int DT, int WT, int VW, int N, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 32 * kNormWarpRows : 1024) norm_row_kernel(
+    const NormArgs a) {
+  using W = Elem<WT>;
+  using C = Chunk<DT, VW>;
+  using raw = typename C::raw;
+  __shared__ float red[2][32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int G = kWarp ? 32 : blockDim.x, tid = kWarp ? lane : threadIdx.x;
+  const int64_t t = kWarp ? blockIdx.x * int64_t(kNormWarpRows) + (threadIdx.x >> 5) : blockIdx.x;
+  if (kWarp && t >= a.T) return;
+  const auto* gamma = static_cast<const typename W::raw*>(a.gamma);
+  const auto* beta = static_cast<const typename W::raw*>(a.beta);
+  const raw* x = static_cast<const raw*>(a.x) + t * a.x_stride;  // may be y: coherent loads
+  raw* y = static_cast<raw*>(a.y) + t * a.H;
+  const float fh = static_cast<float>(a.H);  // divided by: exact for rows of one value
+
+  auto total = [&](float v, int k) {  // over the group, the same bits in every thread
+    v = warp_sum(v);
+    if constexpr (!kWarp) {
+      if (lane == 0) red[k][threadIdx.x >> 5] = v;
+      __syncthreads();
+      v = warp_sum(lane < (G >> 5) ? red[k][lane] : 0.0f);
+    }
+    return v;
+  };
+
+  C c[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int h = (i * G + tid) * VW;
+    if (h < a.H) c[i].load(x + h);
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if ((i * G + tid) * VW < a.H) {
+      float f[VW];
+      c[i].get(f);
+#pragma unroll
+      for (int q = 0; q < VW; ++q) s += f[q];
+    }
+  const float mean = total(s, 0) / fh;
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if ((i * G + tid) * VW < a.H) {
+      float f[VW];
+      c[i].get(f);
+#pragma unroll
+      for (int q = 0; q < VW; ++q) {
+        const float d = f[q] - mean;
+        v = fmaf(d, d, v);
+      }
+    }
+  const float rstd = 1.0f / sqrtf(total(v, 1) / fh + a.eps);
+  if (tid == 0) {
+    if (a.mean) a.mean[t] = mean;
+    if (a.rstd) a.rstd[t] = rstd;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int h = (i * G + tid) * VW;
+    if (h < a.H) {
+      float f[VW], g[VW], b[VW];
+      c[i].get(f);
+#pragma unroll
+      for (int q = 0; q < VW; ++q) g[q] = 1.0f, b[q] = 0.0f;
+      if (gamma) load_weights<WT, VW>(gamma + h, g);
+      if (beta) load_weights<WT, VW>(beta + h, b);
+#pragma unroll
+      for (int q = 0; q < VW; ++q) f[q] = fmaf((f[q] - mean) * rstd, g[q], b[q]);
+      C::put(y + h, f);
+    }
+  }
+}
+
+// Backward: d_x and the CTA's partial sums of the weights' gradients in one pass over x and d_y.
+// A CTA holds R groups of G threads (R = blockDim.x / G; kWarp: G = 32); group j of CTA i takes the
+// tokens i R + j, + gridDim.x R, ..., and reads the next token's rows before it works on this one's.
+// Each thread keeps its columns' gradient sums in registers; at the end the groups add theirs up
+// in order through shared memory.
+constexpr int norm_bwd_threads(int vw, int n, bool warp) {
+  return warp ? 256 : vw * n > 4 ? 512 : 1024;  // what the registers of 8 or 16 columns allow
+}
+template <int DT, int WT, int VW, int N, bool kWarp>
+__global__ void __launch_bounds__(norm_bwd_threads(VW, N, kWarp)) norm_bwd_row_kernel(const NormBwdArgs a,
+                                                                          int G) {
+  using W = Elem<WT>;
+  using C = Chunk<DT, VW>;
+  using raw = typename C::raw;
+  extern __shared__ float sums[];    // [2][H]: the groups' sums (R > 1)
+  __shared__ float2 red[2][32];
+  pdl_wait();
+  pdl_trigger();
+  if constexpr (kWarp) G = 32;
+  const int R = blockDim.x / G;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
+  const auto* gamma = static_cast<const typename W::raw*>(a.gamma);
+  const float fh = static_cast<float>(a.H);
+  float g[N][VW], dg[N][VW], db[N][VW];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int q = 0; q < VW; ++q) g[i][q] = 1.0f, dg[i][q] = 0.0f, db[i][q] = 0.0f;
+    const int h = (i * G + tid) * VW;
+    if (gamma && h < a.H) load_weights<WT, VW>(gamma + h, g[i]);
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * R;
+  int64_t t = blockIdx.x * static_cast<int64_t>(R) + group;
+  C cx[N], cd[N];
+  float mean = 0.f, rstd = 0.f;
+  auto fetch = [&](int64_t at) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int h = (i * G + tid) * VW;
+      if (h < a.H) {
+        cx[i].load_ro(static_cast<const raw*>(a.x) + at * a.x_stride + h);
+        cd[i].load_ro(static_cast<const raw*>(a.dy) + at * a.dy_stride + h);
+      }
+    }
+    mean = a.mean[at];
+    rstd = a.rstd[at];
+  };
+  if (t < a.T) fetch(t);
+  int turn = 0;
+  for (; t < a.T; t += step, turn ^= 1) {
+    float xh[N][VW], q[N][VW], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i * G + tid) * VW < a.H) {
+        cx[i].get(xh[i]);
+        cd[i].get(q[i]);
+#pragma unroll
+        for (int k = 0; k < VW; ++k) {
+          const float d = q[i][k];
+          xh[i][k] = (xh[i][k] - mean) * rstd;
+          dg[i][k] = fmaf(d, xh[i][k], dg[i][k]);
+          db[i][k] += d;
+          q[i][k] = d * g[i][k];
+          s1 += q[i][k];
+          s2 = fmaf(q[i][k], xh[i][k], s2);
+        }
+      }
+    const float r = rstd;
+    if (t + step < a.T) fetch(t + step);
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if constexpr (!kWarp) {
+      const int nw = G >> 5, w0 = group * nw;
+      if (lane == 0) red[turn][warp] = make_float2(s1, s2);
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(G) : "memory");
+      const float2 p = lane < nw ? red[turn][w0 + lane] : make_float2(0.f, 0.f);
+      s1 = warp_sum(p.x);
+      s2 = warp_sum(p.y);
+    }
+    const float c1 = s1 / fh, c2 = s2 / fh;
+    raw* dx = static_cast<raw*>(a.dx) + t * a.H;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int h = (i * G + tid) * VW;
+      if (h < a.H) {
+#pragma unroll
+        for (int k = 0; k < VW; ++k) q[i][k] = r * (q[i][k] - c1 - xh[i][k] * c2);
+        C::put(dx + h, q[i]);
+      }
+    }
+  }
+  if (!a.part) return;
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
+  for (int j = 0; j < R; ++j) {
+    if (j > 0) __syncthreads();
+    if (group != j) continue;
+    float* out = j == R - 1 ? part : sums;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int h = (i * G + tid) * VW;
+      if (h < a.H) {
+#pragma unroll
+        for (int k = 0; k < VW; ++k) {
+          out[h + k] = j > 0 ? sums[h + k] + dg[i][k] : dg[i][k];
+          out[a.H + h + k] = j > 0 ? sums[a.H + h + k] + db[i][k] : db[i][k];
+        }
+      }
+    }
+  }
+}
+
+// Backward for wide rows (16-byte accesses): as above, but the tokens' rows of x and d_y are staged
+// in shared memory by 1-D bulk copies, several tokens ahead, and read from there twice instead of
+// being held in registers, which go to the columns' gradient sums. gamma is kept in shared memory
+// in fp32 (the first and the second four columns of each access apart, so that a warp's 16-byte
+// reads meet no bank twice). The last warp's first lane issues the copies; all waits are bounded,
+// and a group leaves its loop together (named_bar_or).
+template <int DT, int WT, int N>
+__global__ void __launch_bounds__(N == 4 ? 544 : 1024) norm_bwd_ring_kernel(const NormBwdArgs a, int G, int R,
+                                                             int stages) {
+  using E = Elem<DT>;
+  using W = Elem<WT>;
+  using raw = typename E::raw;
+  constexpr int VW = E::kVec;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[8], empty[8];
+  __shared__ float2 red[2][32];
+  const int row_bytes = a.H * static_cast<int>(sizeof(raw));
+  float* gs = reinterpret_cast<float*>(ring + static_cast<size_t>(stages) * 2 * row_bytes);
+  const int n = a.H / VW;  // accesses of a row
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], G / 32);
+    }
+    fence_mbarrier_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+  const auto* gamma = static_cast<const typename W::raw*>(a.gamma);
+  for (int h = threadIdx.x; h < a.H; h += blockDim.x)
+    gs[((h % VW) / 4 * n + h / VW) * 4 + h % 4] = gamma ? W::to_f32(gamma[h]) : 1.0f;
+  __syncthreads();
+
+  if (group >= R) {
+    if (tid == 0) {
+      int64_t issued = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < a.T && ok; t += gridDim.x, ++issued) {
+        const int st = static_cast<int>(issued % stages);
+        if (issued >= stages)
+          ok = mbar_wait(&empty[st], static_cast<uint32_t>((issued / stages - 1) & 1), 130);
+        if (!ok) break;
+        uint8_t* to = ring + static_cast<size_t>(st) * 2 * row_bytes;
+        mbar_arrive_expect_tx(&full[st], 2u * row_bytes);
+        bulk_g2s(to, static_cast<const raw*>(a.x) + t * a.x_stride, row_bytes, &full[st]);
+        bulk_g2s(to + row_bytes, static_cast<const raw*>(a.dy) + t * a.dy_stride, row_bytes,
+                 &full[st]);
+      }
+      if (!ok)  // no copy into this CTA's shared memory may outlive it
+        for (int i = 0; i < stages; ++i) {
+          const int64_t k = issued / stages + (i < issued % stages ? 1 : 0);
+          if (k > 0) mbar_wait(&full[i], static_cast<uint32_t>((k - 1) & 1), 131);
+        }
+    }
+    return;
+  }
+
+  const float fh = static_cast<float>(a.H);
+  float dg[N][VW], db[N][VW];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int q = 0; q < VW; ++q) dg[i][q] = 0.0f, db[i][q] = 0.0f;
+  auto weights = [&](int at, float (&g)[VW]) {
+#pragma unroll
+    for (int q = 0; q < VW; q += 4) {
+      const float4 v = reinterpret_cast<const float4*>(gs)[q / 4 * n + at];
+      g[q] = v.x, g[q + 1] = v.y, g[q + 2] = v.z, g[q + 3] = v.w;
+    }
+  };
+  int64_t k = group;
+  int64_t t = blockIdx.x + k * static_cast<int64_t>(gridDim.x);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * R;
+  float mean = 0.f, rstd = 0.f;
+  if (t < a.T) mean = a.mean[t], rstd = a.rstd[t];
+  int turn = 0;
+  for (; t < a.T; t += step, k += R, turn ^= 1) {
+    const int st = static_cast<int>(k % stages);
+    const float m = mean, r = rstd;
+    if (t + step < a.T) mean = a.mean[t + step], rstd = a.rstd[t + step];
+    const bool ok = mbar_wait(&full[st], static_cast<uint32_t>((k / stages) & 1), 132);
+    const uint4* sx = reinterpret_cast<const uint4*>(ring + static_cast<size_t>(st) * 2 * row_bytes);
+    const uint4* sd = sx + n;
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = i * G + tid;
+      if (at < n) {
+        float x[VW], d[VW], g[VW];
+        E::unpack(sx[at], x);
+        E::unpack(sd[at], d);
+        weights(at, g);
+#pragma unroll
+        for (int q = 0; q < VW; ++q) {
+          const float xh = (x[q] - m) * r;
+          dg[i][q] = fmaf(d[q], xh, dg[i][q]);
+          db[i][q] += d[q];
+          const float v = d[q] * g[q];
+          s1 += v;
+          s2 = fmaf(v, xh, s2);
+        }
+      }
+    }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if (lane == 0) red[turn][warp] = make_float2(s1, s2);
+    if (named_bar_or(group + 1, G, !ok)) break;
+    const int nw = G >> 5;
+    const float2 p = lane < nw ? red[turn][group * nw + lane] : make_float2(0.f, 0.f);
+    const float c1 = warp_sum(p.x) / fh, c2 = warp_sum(p.y) / fh;
+    raw* dx = static_cast<raw*>(a.dx) + t * a.H;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = i * G + tid;
+      if (at < n) {
+        float x[VW], d[VW], g[VW];
+        E::unpack(sx[at], x);
+        E::unpack(sd[at], d);
+        weights(at, g);
+#pragma unroll
+        for (int q = 0; q < VW; ++q) x[q] = r * (d[q] * g[q] - c1 - (x[q] - m) * r * c2);
+        st_stream(dx + at * VW, E::pack(x));
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+  }
+  if (!a.part) return;
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
+  float* sums = reinterpret_cast<float*>(ring);  // the stages are free: every group is done
+  for (int j = 0; j < R; ++j) {
+    if (R > 1) asm volatile("bar.sync 15, %0;" ::"r"(R * G) : "memory");
+    if (group != j) continue;
+    float* out = j == R - 1 ? part : sums;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = i * G + tid;
+      if (at < n) {
+#pragma unroll
+        for (int q = 0; q < VW; ++q) {
+          const int h = at * VW + q;
+          out[h] = j > 0 ? sums[h] + dg[i][q] : dg[i][q];
+          out[a.H + h] = j > 0 ? sums[a.H + h] + db[i][q] : db[i][q];
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ any row
 
 constexpr int kNormThreads = 256;
 
@@ -177,26 +570,151 @@ unsigned row_grid(int64_t T) {
   return static_cast<unsigned>(T < cap ? T : cap);
 }
 
+bool vector_rows(int vec, int64_t H, std::initializer_list<int64_t> strides,
+                 std::initializer_list<const void*> arrays) {
+  if (H % vec != 0) return false;
+  for (const int64_t st : strides)
+    if (st % vec != 0) return false;
+  for (const void* p : arrays)
+    if (!aligned16(p)) return false;
+  return true;
+}
+
+int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
+
+template <int DT, int WT, int VW>
+cudaError_t norm_forward_rows(const NormArgs& a, cudaStream_t s, bool* done) {
+  const int64_t n = a.H / VW;  // accesses of a row (VW divides H)
+  *done = true;
+  const bool few = a.T < 2 * device_sm_count();
+  if (!few && n <= 256) {
+    // A warp per row: no barrier, and the rows of 16 or more warps in flight per SM.
+    const dim3 grid(static_cast<unsigned>((a.T + kNormWarpRows - 1) / kNormWarpRows));
+    const dim3 block(32 * kNormWarpRows);
+    auto k = n <= 32    ? norm_row_kernel<DT, WT, VW, 1, true>
+             : n <= 64  ? norm_row_kernel<DT, WT, VW, 2, true>
+             : n <= 128 ? norm_row_kernel<DT, WT, VW, 4, true>
+                        : norm_row_kernel<DT, WT, VW, 8, true>;
+    return launch_pdl(k, grid, block, 0, s, a);
+  }
+  // A CTA per row; with few rows as many threads as the row has work for.
+  const int per = few && n <= 1024 ? 1 : n <= 2048 && few ? 2 : 4;
+  const int G = round32((n + per - 1) / per);
+  if (G <= 1024) {
+    auto k = per == 1   ? norm_row_kernel<DT, WT, VW, 1, false>
+             : per == 2 ? norm_row_kernel<DT, WT, VW, 2, false>
+                        : norm_row_kernel<DT, WT, VW, 4, false>;
+    return launch_pdl(k, dim3(static_cast<unsigned>(a.T)), dim3(G), 0, s, a);
+  }
+  *done = false;
+  return cudaSuccess;
+}
+
 template <int DT, int WT>
 int norm_forward(const NormArgs& a, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(norm_loop_kernel<DT, WT>, dim3(row_grid(a.T)),
-                                   dim3(kNormThreads), 0, s, a);
+  constexpr int VE = Elem<DT>::kVec;
+  bool done = false;
+  cudaError_t e;
+  if (vector_rows(VE, a.H, {a.x_stride}, {a.x, a.y, a.gamma, a.beta}))
+    e = norm_forward_rows<DT, WT, VE>(a, s, &done);
+  else
+    e = norm_forward_rows<DT, WT, 1>(a, s, &done);
+  if (!done)
+    e = launch_pdl(norm_loop_kernel<DT, WT>, dim3(row_grid(a.T)), dim3(kNormThreads), 0, s, a);
   note_launches(1);
   return e == cudaSuccess ? 0 : MHC_ERR_CUDA;
 }
 
+// CTAs of a backward kernel: as many as are resident, no more than tokens or partial rows.
+unsigned norm_bwd_grid(const void* kernel, int threads, size_t smem, int64_t groups_of_tokens) {
+  int resident = 1;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, smem) !=
+          cudaSuccess ||
+      resident < 1)
+    resident = 1;
+  int64_t grid = static_cast<int64_t>(device_sm_count()) * resident;
+  if (grid > kNormPartRows) grid = kNormPartRows;
+  if (grid > groups_of_tokens) grid = groups_of_tokens;
+  return static_cast<unsigned>(grid);
+}
+
+// Launches the register form and returns its number of partial rows, or 0 (nothing launched) where
+// the row is too wide for it.
+template <int DT, int WT, int VW>
+int norm_backward_rows(const NormBwdArgs& a, cudaStream_t s, cudaError_t* e) {
+  const int64_t n = a.H / VW;
+  const bool warp = n <= 64;
+  int per = 1;
+  while (per < 4 && (warp ? n > 32 * per : n > norm_bwd_threads(VW, per, false) * per)) per *= 2;
+  if (VW > 1 && per > 2) return 0;
+  const int G = warp ? 32 : round32((n + per - 1) / per);
+  if (G > norm_bwd_threads(VW, per, false)) return 0;
+  const int R = warp ? 8 : G >= 256 ? 1 : G >= 160 ? 2 : G >= 96 ? 4 : 8;
+  auto k = warp ? (per == 1 ? norm_bwd_row_kernel<DT, WT, VW, 1, true>
+                            : norm_bwd_row_kernel<DT, WT, VW, 2, true>)
+           : per == 1 ? norm_bwd_row_kernel<DT, WT, VW, 1, false>
+           : per == 2 ? norm_bwd_row_kernel<DT, WT, VW, 2, false>
+                      : norm_bwd_row_kernel<DT, WT, VW, (VW == 1 ? 4 : 1), false>;
+  const size_t smem = R > 1 ? static_cast<size_t>(2) * a.H * 4 : 0;
+  const unsigned grid =
+      norm_bwd_grid(reinterpret_cast<const void*>(k), G * R, smem, (a.T + R - 1) / R);
+  *e = launch_pdl(k, dim3(grid), dim3(G * R), smem, s, a, G);
+  note_launches(1);
+  return static_cast<int>(grid);
+}
+
+// The staged form, likewise: rows of 16-byte accesses.
 template <int DT, int WT>
-int norm_backward(const NormBwdArgs& a, float* dgamma, float* dbeta, cudaStream_t s) {
-  cudaError_t e = launch_pdl(norm_bwd_dx_loop_kernel<DT, WT>, dim3(row_grid(a.T)),
-                             dim3(kNormThreads), 0, s, a);
+int norm_backward_ring(const NormBwdArgs& a, cudaStream_t s, cudaError_t* e) {
+  const int64_t n = a.H / Elem<DT>::kVec;
+  if (n > 512 * 4) return 0;
+  const int per = n > 2 * 992 ? 4 : n > 330 ? 2 : 1;
+  const int G = round32((n + per - 1) / per);
+  const int R = per == 4 || G > 496 ? 1 : G > 330 ? 2 : 3;
+  const size_t row = static_cast<size_t>(a.H) * sizeof(typename Elem<DT>::raw);
+  const size_t limit = 224 * 1024 - static_cast<size_t>(a.H) * 4;
+  const int stages = static_cast<int>(limit / (2 * row) < 8 ? limit / (2 * row) : 8);
+  if (stages < 2) return 0;
+  const size_t smem = stages * 2 * row + static_cast<size_t>(a.H) * 4;
+  auto k = per == 1   ? norm_bwd_ring_kernel<DT, WT, 1>
+           : per == 2 ? norm_bwd_ring_kernel<DT, WT, 2>
+                      : norm_bwd_ring_kernel<DT, WT, 4>;
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(k), static_cast<int>(smem))) return 0;
+  const unsigned grid =
+      norm_bwd_grid(reinterpret_cast<const void*>(k), G * R + 32, smem, a.T);
+  *e = launch_pdl(k, dim3(grid), dim3(G * R + 32), smem, s, a, G, R, stages);
   note_launches(1);
+  return static_cast<int>(grid);
+}
+
+template <int DT, int WT>
+int norm_backward(NormBwdArgs a, float* dgamma, float* dbeta, cudaStream_t s) {
+  constexpr int VE = Elem<DT>::kVec;
+  const bool params = dgamma || dbeta;
+  if (!params) a.part = nullptr;
+  cudaError_t e = cudaSuccess;
+  int rows = 0;
+  if (vector_rows(VE, a.H, {a.x_stride, a.dy_stride}, {a.x, a.dy, a.dx, a.gamma})) {
+    if (a.H >= 2048) rows = norm_backward_ring<DT, WT>(a, s, &e);
+    if (rows == 0) rows = norm_backward_rows<DT, WT, VE>(a, s, &e);
+  } else {
+    rows = norm_backward_rows<DT, WT, 1>(a, s, &e);
+  }
+  if (rows == 0) {
+    e = launch_pdl(norm_bwd_dx_loop_kernel<DT, WT>, dim3(row_grid(a.T)), dim3(kNormThreads), 0, s,
+                   a);
+    note_launches(1);
+    if (e != cudaSuccess) return MHC_ERR_CUDA;
+    if (params) {
+      rows = norm_part_rows(a.T);
+      e = launch_pdl(norm_bwd_part_loop_kernel<DT>,
+                     dim3((a.H + kNormThreads - 1) / kNormThreads, rows), dim3(kNormThreads), 0, s,
+                     a);
+      note_launches(1);
+    }
+  }
   if (e != cudaSuccess) return MHC_ERR_CUDA;
-  if (!dgamma && !dbeta) return 0;
-  const int rows = norm_part_rows(a.T);
-  e = launch_pdl(norm_bwd_part_loop_kernel<DT>, dim3((a.H + kNormThreads - 1) / kNormThreads, rows),
-                 dim3(kNormThreads), 0, s, a);
-  note_launches(1);
-  if (e != cudaSuccess) return MHC_ERR_CUDA;
+  if (!params) return 0;
   e = launch_pdl(norm_bwd_sum_kernel, dim3(static_cast<unsigned>((2 * int64_t(a.H) + 31) / 32)),
                  dim3(256), 0, s, static_cast<const float*>(a.part), rows, int64_t(a.H), dgamma,
                  dbeta);

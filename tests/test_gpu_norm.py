@@ -12,7 +12,8 @@ from rows_util import DTYPES, check, f64, norm_bounds, norm_bwd_bounds, rounded
 pytestmark = pytest.mark.gpu
 
 SHAPES = [(1, 1), (1, 7168), (3, 7), (5, 127), (64, 512), (33, 1000), (9, 1001), (4, 8192),
-          (3, 16392), (200, 64), (1000, 1032), (300, 2048), (2, 40000), (700, 96)]
+          (3, 16392), (200, 64), (1000, 1032), (300, 2048), (2, 40000), (700, 96), (301, 7168),
+          (400, 4096), (310, 16384), (1200, 520), (900, 264), (3, 5000), (333, 3001), (300, 32768)]
 
 
 def _make(T, H, dtype, weights, seed, gap=0, offset=0.3):
