@@ -77,13 +77,25 @@ struct Chunk {
   }
 };
 
-// VW weights at p (of the rows' type or fp32), through L1.
+// VW weights at p (of the rows' type or fp32), through L1. wide: p is 32-byte aligned; eight fp32
+// weights then come in one access (two of 16 bytes each touch every sector of the warp's span, which
+// made the weights' L1 traffic the forward pass's bound).
 template <int WT, int VW>
-__device__ __forceinline__ void load_weights(const typename Elem<WT>::raw* p, float (&g)[VW]) {
+__device__ __forceinline__ void load_weights(const typename Elem<WT>::raw* p, bool wide,
+                                             float (&g)[VW]) {
   using W = Elem<WT>;
   if constexpr (VW == 1) {
     g[0] = W::to_f32(__ldg(p));
   } else {
+    if constexpr (WT == 2 && VW == 8) {
+      if (wide) {
+        asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(g[0]), "=f"(g[1]), "=f"(g[2]), "=f"(g[3]), "=f"(g[4]), "=f"(g[5]),
+                       "=f"(g[6]), "=f"(g[7])
+                     : "l"(p));
+        return;
+      }
+    }
 #pragma unroll
     for (int q = 0; q < VW; q += W::kVec) {
       float x[W::kVec];
@@ -93,85 +105,125 @@ __device__ __forceinline__ void load_weights(const typename Elem<WT>::raw* p, fl
     }
   }
 }
+__device__ __forceinline__ bool aligned32(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
+}
 
 constexpr int kNormWarpRows = 4;  // rows per CTA of the one-warp-per-row forward form
 
-// Forward. kWarp: a warp per row, no barrier; otherwise the CTA holds one row (blockDim.x = G).
-template <int DT, int WT, int VW, int N, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 32 * kNormWarpRows : 1024) norm_row_kernel(
+// Forward. kWarp: a warp per K rows, no barrier; otherwise a CTA (G = blockDim.x threads) per K
+// rows. Two rows at a time read the weights once and share each exchange between threads.
+template <int DT, int WT, int VW, int N, int K, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 32 * kNormWarpRows : K == 2 ? 512 : 1024) norm_row_kernel(
     const NormArgs a) {
   using W = Elem<WT>;
   using C = Chunk<DT, VW>;
   using raw = typename C::raw;
-  __shared__ float red[2][32];
+  static_assert(K == 1 || K == 2, "one or two rows at a time");
+  __shared__ float red[2][64];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = kWarp ? 32 : blockDim.x, tid = kWarp ? lane : threadIdx.x;
-  const int64_t t = kWarp ? blockIdx.x * int64_t(kNormWarpRows) + (threadIdx.x >> 5) : blockIdx.x;
-  if (kWarp && t >= a.T) return;
+  const int64_t t0 =
+      K * (kWarp ? blockIdx.x * int64_t(kNormWarpRows) + warp : static_cast<int64_t>(blockIdx.x));
+  if (kWarp && t0 >= a.T) return;
+  const int rows = K == 2 && t0 + 1 < a.T ? 2 : 1;
   const auto* gamma = static_cast<const typename W::raw*>(a.gamma);
   const auto* beta = static_cast<const typename W::raw*>(a.beta);
-  const raw* x = static_cast<const raw*>(a.x) + t * a.x_stride;  // may be y: coherent loads
-  raw* y = static_cast<raw*>(a.y) + t * a.H;
+  const bool gw = aligned32(gamma), bw = aligned32(beta);
+  const raw* x = static_cast<const raw*>(a.x) + t0 * a.x_stride;  // may be y: coherent loads
+  raw* y = static_cast<raw*>(a.y) + t0 * a.H;
   const float fh = static_cast<float>(a.H);  // divided by: exact for rows of one value
 
-  auto total = [&](float v, int k) {  // over the group, the same bits in every thread
-    v = warp_sum(v);
-    if constexpr (!kWarp) {
-      if (lane == 0) red[k][threadIdx.x >> 5] = v;
-      __syncthreads();
-      v = warp_sum(lane < (G >> 5) ? red[k][lane] : 0.0f);
+  // Sums over the group, the same bits in every thread.
+  auto total = [&](const float (&v)[K], int turn, float (&out)[K]) {
+    if constexpr (K == 1) {
+      out[0] = warp_sum(v[0]);
+      if constexpr (!kWarp) {
+        if (lane == 0) red[turn][warp] = out[0];
+        __syncthreads();
+        out[0] = warp_sum(lane < (G >> 5) ? red[turn][lane] : 0.0f);
+      }
+    } else {
+      const float h = warp_sum_halves(v[0], v[1]);
+      float2 p;
+      if constexpr (kWarp) {
+        p = join_halves(h);
+      } else {
+        if ((lane & 15) == 0) red[turn][2 * lane + warp] = h;
+        __syncthreads();
+        p = sum_of_warps(red[turn], G >> 5);
+      }
+      out[0] = p.x, out[1] = p.y;
     }
-    return v;
   };
 
-  C c[N];
+  C c[K][N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int h = (i * G + tid) * VW;
-    if (h < a.H) c[i].load(x + h);
-  }
-  float s = 0.f;
+  for (int k = 0; k < K; ++k)
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if ((i * G + tid) * VW < a.H) {
-      float f[VW];
-      c[i].get(f);
-#pragma unroll
-      for (int q = 0; q < VW; ++q) s += f[q];
+    for (int i = 0; i < N; ++i) {
+      const int h = (i * G + tid) * VW;
+      if (h < a.H && k < rows) c[k][i].load(x + k * a.x_stride + h);
     }
-  const float mean = total(s, 0) / fh;
-  float v = 0.f;
+  float s[K], mean[K], v[K], rstd[K];
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if ((i * G + tid) * VW < a.H) {
-      float f[VW];
-      c[i].get(f);
+  for (int k = 0; k < K; ++k) {
+    s[k] = 0.f;
 #pragma unroll
-      for (int q = 0; q < VW; ++q) {
-        const float d = f[q] - mean;
-        v = fmaf(d, d, v);
+    for (int i = 0; i < N; ++i)
+      if ((i * G + tid) * VW < a.H && k < rows) {
+        float f[VW];
+        c[k][i].get(f);
+#pragma unroll
+        for (int q = 0; q < VW; ++q) s[k] += f[q];
       }
+  }
+  total(s, 0, mean);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    mean[k] /= fh;
+    v[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i * G + tid) * VW < a.H && k < rows) {
+        float f[VW];
+        c[k][i].get(f);
+#pragma unroll
+        for (int q = 0; q < VW; ++q) {
+          const float d = f[q] - mean[k];
+          v[k] = fmaf(d, d, v[k]);
+        }
+      }
+  }
+  total(v, 1, rstd);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    rstd[k] = 1.0f / sqrtf(rstd[k] / fh + a.eps);
+    if (tid == 0 && k < rows) {
+      if (a.mean) a.mean[t0 + k] = mean[k];
+      if (a.rstd) a.rstd[t0 + k] = rstd[k];
     }
-  const float rstd = 1.0f / sqrtf(total(v, 1) / fh + a.eps);
-  if (tid == 0) {
-    if (a.mean) a.mean[t] = mean;
-    if (a.rstd) a.rstd[t] = rstd;
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int h = (i * G + tid) * VW;
     if (h < a.H) {
-      float f[VW], g[VW], b[VW];
-      c[i].get(f);
+      float g[VW], b[VW];
 #pragma unroll
       for (int q = 0; q < VW; ++q) g[q] = 1.0f, b[q] = 0.0f;
-      if (gamma) load_weights<WT, VW>(gamma + h, g);
-      if (beta) load_weights<WT, VW>(beta + h, b);
+      if (gamma) load_weights<WT, VW>(gamma + h, gw, g);
+      if (beta) load_weights<WT, VW>(beta + h, bw, b);
 #pragma unroll
-      for (int q = 0; q < VW; ++q) f[q] = fmaf((f[q] - mean) * rstd, g[q], b[q]);
-      C::put(y + h, f);
+      for (int k = 0; k < K; ++k)
+        if (k < rows) {
+          float f[VW];
+          c[k][i].get(f);
+#pragma unroll
+          for (int q = 0; q < VW; ++q) f[q] = fmaf((f[q] - mean[k]) * rstd[k], g[q], b[q]);
+          C::put(y + k * static_cast<int64_t>(a.H) + h, f);
+        }
     }
   }
 }
@@ -191,7 +243,7 @@ __global__ void __launch_bounds__(norm_bwd_threads(VW, N, kWarp)) norm_bwd_row_k
   using C = Chunk<DT, VW>;
   using raw = typename C::raw;
   extern __shared__ float sums[];    // [2][H]: the groups' sums (R > 1)
-  __shared__ float2 red[2][32];
+  __shared__ float red[2][64];  // by turn: each warp's two sums (sum_of_warps)
   pdl_wait();
   pdl_trigger();
   if constexpr (kWarp) G = 32;
@@ -206,7 +258,7 @@ __global__ void __launch_bounds__(norm_bwd_threads(VW, N, kWarp)) norm_bwd_row_k
 #pragma unroll
     for (int q = 0; q < VW; ++q) g[i][q] = 1.0f, dg[i][q] = 0.0f, db[i][q] = 0.0f;
     const int h = (i * G + tid) * VW;
-    if (gamma && h < a.H) load_weights<WT, VW>(gamma + h, g[i]);
+    if (gamma && h < a.H) load_weights<WT, VW>(gamma + h, aligned32(gamma), g[i]);
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * R;
   int64_t t = blockIdx.x * static_cast<int64_t>(R) + group;
@@ -246,17 +298,17 @@ __global__ void __launch_bounds__(norm_bwd_threads(VW, N, kWarp)) norm_bwd_row_k
       }
     const float r = rstd;
     if (t + step < a.T) fetch(t + step);
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if constexpr (!kWarp) {
+    const float half = warp_sum_halves(s1, s2);
+    float2 p;
+    if constexpr (kWarp) {
+      p = join_halves(half);
+    } else {
       const int nw = G >> 5, w0 = group * nw;
-      if (lane == 0) red[turn][warp] = make_float2(s1, s2);
+      if ((lane & 15) == 0) red[turn][2 * lane + warp] = half;
       asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(G) : "memory");
-      const float2 p = lane < nw ? red[turn][w0 + lane] : make_float2(0.f, 0.f);
-      s1 = warp_sum(p.x);
-      s2 = warp_sum(p.y);
+      p = sum_of_warps(red[turn] + w0, nw);
     }
-    const float c1 = s1 / fh, c2 = s2 / fh;
+    const float c1 = p.x / fh, c2 = p.y / fh;
     raw* dx = static_cast<raw*>(a.dx) + t * a.H;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -303,7 +355,7 @@ __global__ void __launch_bounds__(N == 4 ? 544 : 1024) norm_bwd_ring_kernel(cons
   constexpr int VW = E::kVec;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[8], empty[8];
-  __shared__ float2 red[2][32];
+  __shared__ float red[2][64];  // by turn: each warp's two sums (sum_of_warps)
   const int row_bytes = a.H * static_cast<int>(sizeof(raw));
   float* gs = reinterpret_cast<float*>(ring + static_cast<size_t>(stages) * 2 * row_bytes);
   const int n = a.H / VW;  // accesses of a row
@@ -348,92 +400,116 @@ __global__ void __launch_bounds__(N == 4 ? 544 : 1024) norm_bwd_ring_kernel(cons
   }
 
   const float fh = static_cast<float>(a.H);
-  float dg[N][VW], db[N][VW];
+  constexpr int P = VW / 2;  // pairs of an access
+  F2 dg[N][P], db[N][P];
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int q = 0; q < VW; ++q) dg[i][q] = 0.0f, db[i][q] = 0.0f;
-  auto weights = [&](int at, float (&g)[VW]) {
+    for (int q = 0; q < P; ++q) dg[i][q] = f2(0.0f), db[i][q] = f2(0.0f);
+  // The access at `at` of the staged rows, in pairs: x - mean, d_y and d_y gamma.
+  auto take = [&](const uint4* sx, const uint4* sd, int at, F2 neg_mean, F2 (&xm)[P], F2 (&d)[P],
+                  F2 (&v)[P]) {
+    float f[VW];
+    E::unpack(sx[at], f);
+#pragma unroll
+    for (int q = 0; q < P; ++q) xm[q] = f2(f[2 * q], f[2 * q + 1]) + neg_mean;
+    E::unpack(sd[at], f);
+#pragma unroll
+    for (int q = 0; q < P; ++q) d[q] = f2(f[2 * q], f[2 * q + 1]);
 #pragma unroll
     for (int q = 0; q < VW; q += 4) {
-      const float4 v = reinterpret_cast<const float4*>(gs)[q / 4 * n + at];
-      g[q] = v.x, g[q + 1] = v.y, g[q + 2] = v.z, g[q + 3] = v.w;
+      const float4 g = reinterpret_cast<const float4*>(gs)[q / 4 * n + at];
+      v[q / 2] = d[q / 2] * f2(g.x, g.y);
+      v[q / 2 + 1] = d[q / 2 + 1] * f2(g.z, g.w);
     }
   };
   int64_t k = group;
   int64_t t = blockIdx.x + k * static_cast<int64_t>(gridDim.x);
   const int64_t step = static_cast<int64_t>(gridDim.x) * R;
+  const int nw = G >> 5;
   float mean = 0.f, rstd = 0.f;
   if (t < a.T) mean = a.mean[t], rstd = a.rstd[t];
   int turn = 0;
   for (; t < a.T; t += step, k += R, turn ^= 1) {
     const int st = static_cast<int>(k % stages);
-    const float m = mean, r = rstd;
+    const F2 neg_mean = f2(-mean);
+    const float r = rstd;
     if (t + step < a.T) mean = a.mean[t + step], rstd = a.rstd[t + step];
     const bool ok = mbar_wait(&full[st], static_cast<uint32_t>((k / stages) & 1), 132);
     const uint4* sx = reinterpret_cast<const uint4*>(ring + static_cast<size_t>(st) * 2 * row_bytes);
     const uint4* sd = sx + n;
-    float s1 = 0.f, s2 = 0.f;
+    F2 s1 = f2(0.f), s2 = f2(0.f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int at = i * G + tid;
       if (at < n) {
-        float x[VW], d[VW], g[VW];
-        E::unpack(sx[at], x);
-        E::unpack(sd[at], d);
-        weights(at, g);
+        F2 xm[P], d[P], v[P];
+        take(sx, sd, at, neg_mean, xm, d, v);
 #pragma unroll
-        for (int q = 0; q < VW; ++q) {
-          const float xh = (x[q] - m) * r;
-          dg[i][q] = fmaf(d[q], xh, dg[i][q]);
-          db[i][q] += d[q];
-          const float v = d[q] * g[q];
-          s1 += v;
-          s2 = fmaf(v, xh, s2);
+        for (int q = 0; q < P; ++q) {
+          const F2 xh = xm[q] * f2(r);
+          dg[i][q] = fma2(d[q], xh, dg[i][q]);
+          db[i][q] = db[i][q] + d[q];
+          s1 = s1 + v[q];
+          s2 = fma2(v[q], xh, s2);
         }
       }
     }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if (lane == 0) red[turn][warp] = make_float2(s1, s2);
+    const float2 u1 = split(s1), u2 = split(s2);
+    const float half = warp_sum_halves(u1.x + u1.y, u2.x + u2.y);
+    if ((lane & 15) == 0) red[turn][2 * lane + warp] = half;
     if (named_bar_or(group + 1, G, !ok)) break;
-    const int nw = G >> 5;
-    const float2 p = lane < nw ? red[turn][group * nw + lane] : make_float2(0.f, 0.f);
-    const float c1 = warp_sum(p.x) / fh, c2 = warp_sum(p.y) / fh;
+    const float2 p = sum_of_warps(red[turn] + group * nw, nw);
+    // d_x = r v - r c1 - (x - mean) r^2 c2
+    const F2 fr = f2(r), f1 = f2(-r * (p.x / fh)), fx = f2(-r * r * (p.y / fh));
     raw* dx = static_cast<raw*>(a.dx) + t * a.H;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int at = i * G + tid;
       if (at < n) {
-        float x[VW], d[VW], g[VW];
-        E::unpack(sx[at], x);
-        E::unpack(sd[at], d);
-        weights(at, g);
+        F2 xm[P], d[P], v[P];
+        take(sx, sd, at, neg_mean, xm, d, v);
+        float o[VW];
 #pragma unroll
-        for (int q = 0; q < VW; ++q) x[q] = r * (d[q] * g[q] - c1 - (x[q] - m) * r * c2);
-        st_stream(dx + at * VW, E::pack(x));
+        for (int q = 0; q < P; ++q) {
+          const float2 u = split(fma2(v[q], fr, fma2(xm[q], fx, f1)));
+          o[2 * q] = u.x, o[2 * q + 1] = u.y;
+        }
+        st_stream(dx + at * VW, E::pack(o));
       }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
   }
   if (!a.part) return;
-  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
-  float* sums = reinterpret_cast<float*>(ring);  // the stages are free: every group is done
+  // The groups' sums, in order: through the stages' memory (free: every group is done), each
+  // access's first and second four columns apart as gamma's.
+  float4* part = reinterpret_cast<float4*>(a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H);
+  float4* sums = reinterpret_cast<float4*>(ring);
   for (int j = 0; j < R; ++j) {
     if (R > 1) asm volatile("bar.sync 15, %0;" ::"r"(R * G) : "memory");
     if (group != j) continue;
-    float* out = j == R - 1 ? part : sums;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int at = i * G + tid;
       if (at < n) {
 #pragma unroll
-        for (int q = 0; q < VW; ++q) {
-          const int h = at * VW + q;
-          out[h] = j > 0 ? sums[h] + dg[i][q] : dg[i][q];
-          out[a.H + h] = j > 0 ? sums[a.H + h] + db[i][q] : db[i][q];
-        }
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int q = 0; q < P; q += 2) {
+            const float2 lo = split(w == 0 ? dg[i][q] : db[i][q]);
+            const float2 hi = split(w == 0 ? dg[i][q + 1] : db[i][q + 1]);
+            float4 v = make_float4(lo.x, lo.y, hi.x, hi.y);
+            float4* sum = sums + (w * (P / 2) + q / 2) * n + at;
+            if (j > 0) {
+              const float4 b = *sum;
+              v = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
+            }
+            if (j < R - 1)
+              *sum = v;
+            else
+              part[(w * a.H + at * VW) / 4 + q / 2] = v;
+          }
       }
     }
   }
@@ -588,23 +664,25 @@ cudaError_t norm_forward_rows(const NormArgs& a, cudaStream_t s, bool* done) {
   *done = true;
   const bool few = a.T < 2 * device_sm_count();
   if (!few && n <= 256) {
-    // A warp per row: no barrier, and the rows of 16 or more warps in flight per SM.
-    const dim3 grid(static_cast<unsigned>((a.T + kNormWarpRows - 1) / kNormWarpRows));
-    const dim3 block(32 * kNormWarpRows);
-    auto k = n <= 32    ? norm_row_kernel<DT, WT, VW, 1, true>
-             : n <= 64  ? norm_row_kernel<DT, WT, VW, 2, true>
-             : n <= 128 ? norm_row_kernel<DT, WT, VW, 4, true>
-                        : norm_row_kernel<DT, WT, VW, 8, true>;
-    return launch_pdl(k, grid, block, 0, s, a);
+    // A warp per row or two: no barrier.
+    auto k = n <= 32    ? norm_row_kernel<DT, WT, VW, 1, 2, true>
+             : n <= 64  ? norm_row_kernel<DT, WT, VW, 2, 2, true>
+             : n <= 128 ? norm_row_kernel<DT, WT, VW, 4, 2, true>
+                        : norm_row_kernel<DT, WT, VW, 8, 1, true>;
+    const int rows = kNormWarpRows * (n <= 128 ? 2 : 1);
+    return launch_pdl(k, dim3(static_cast<unsigned>((a.T + rows - 1) / rows)),
+                      dim3(32 * kNormWarpRows), 0, s, a);
   }
-  // A CTA per row; with few rows as many threads as the row has work for.
-  const int per = few && n <= 1024 ? 1 : n <= 2048 && few ? 2 : 4;
+  // A CTA per two rows; with few rows one each, and as many threads as the row has work for.
+  const int per = few && n <= 1024 ? 1 : few && n <= 2048 ? 2 : 4;
   const int G = round32((n + per - 1) / per);
   if (G <= 1024) {
-    auto k = per == 1   ? norm_row_kernel<DT, WT, VW, 1, false>
-             : per == 2 ? norm_row_kernel<DT, WT, VW, 2, false>
-                        : norm_row_kernel<DT, WT, VW, 4, false>;
-    return launch_pdl(k, dim3(static_cast<unsigned>(a.T)), dim3(G), 0, s, a);
+    auto k = per == 1   ? norm_row_kernel<DT, WT, VW, 1, 1, false>
+             : per == 2 ? norm_row_kernel<DT, WT, VW, 2, 1, false>
+             : few || G > 512 ? norm_row_kernel<DT, WT, VW, 4, 1, false>
+                              : norm_row_kernel<DT, WT, VW, 4, 2, false>;
+    const int64_t grid = per < 4 || few || G > 512 ? a.T : (a.T + 1) / 2;
+    return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(G), 0, s, a);
   }
   *done = false;
   return cudaSuccess;

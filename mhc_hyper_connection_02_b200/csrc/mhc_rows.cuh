@@ -131,6 +131,41 @@ __device__ __forceinline__ uint4 load_window(const typename Elem<DT>::raw* row, 
   return w;
 }
 
+// ------------------------------------------------------------------------------ pairs
+//
+// Two fp32 operations in one instruction (each rounded as on its own): half the issue slots where
+// a loop over elements is bound by them.
+
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // ------------------------------------------------------------------------------ reductions
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -142,6 +177,31 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Both sums in five exchanges: lanes 0-15 end with the sum of a, lanes 16-31 with that of b.
+__device__ __forceinline__ float warp_sum_halves(float a, float b) {
+  const bool high = (threadIdx.x & 16) != 0;
+  float v = high ? b : a;
+  v += __shfl_xor_sync(0xffffffffu, high ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// (sum of a, sum of b) in every lane, from warp_sum_halves' result.
+__device__ __forceinline__ float2 join_halves(float v) {
+  const float o = __shfl_xor_sync(0xffffffffu, v, 16);
+  return (threadIdx.x & 16) != 0 ? make_float2(o, v) : make_float2(v, o);
+}
+// The pair of sums over nw warps from their halves in red[0 .. nw) and red[32 .. 32 + nw).
+__device__ __forceinline__ float2 sum_of_warps(const float* red, int nw) {
+  const int half = (threadIdx.x >> 4) & 1, l = threadIdx.x & 15;
+  const float* r = red + 32 * half;
+  float v = l < nw ? r[l] : 0.0f;
+  if (l + 16 < nw) v += r[l + 16];
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return join_halves(v);
 }
 
 // Block reductions of NT threads: an xor tree in each warp, then the warps in order, the same bits
