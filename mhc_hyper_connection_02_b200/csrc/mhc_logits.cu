@@ -27,11 +27,8 @@
 
 namespace mhc {
 
-constexpr int kLgThreads = 256;
 constexpr int kLgUnroll = 4;
 constexpr int kLgTopMax = MHC_TOP_MAX;
-constexpr int kLgCand = 1024;     // candidates for the top alternatives kept in shared memory
-constexpr int kLgTeacherMax = MHC_DISTILL_MAX;
 constexpr float kDCut = -200.0f;  // 2^-200 is zero in fp32: cutting d there keeps 0 * d finite
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -39,6 +36,22 @@ __device__ __forceinline__ float ex2(float d) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d));
   return e;
+}
+
+__device__ __forceinline__ F2 ex2(F2 d) {
+  const float2 v = split(d);
+  return f2(ex2(v.x), ex2(v.y));
+}
+__device__ __forceinline__ F2 max2(F2 d, float lo) {
+  const float2 v = split(d);
+  return f2(fmaxf(v.x, lo), fmaxf(v.y, lo));
+}
+
+// May Elem's cut of the logits at -2^100 stand for the cut of d? Where c carries that value far
+// below kDCut, but not to -infinity.
+template <int DT>
+__device__ __forceinline__ bool cut_ok(float c) {
+  return !Elem<DT>::kCuts || (c > 1e-18f && c < 1e7f);
 }
 
 // May d be formed as fma(z, c, -mc)? While mc's rounding stays far below one.
@@ -70,59 +83,80 @@ __device__ __forceinline__ RowPart row_part(const void* row, int n, int rank, in
   return p;
 }
 
-// This thread's sums over its windows of the part: first + tid, + kLgThreads, .... The usual d is
-// one fma, z c - mc with mc = m c rounded: every d is off by mc's rounding, which the end takes out
-// again. Where mc overflows (the lowest finite values, or an infinity) d is (z - m) c.
-template <int DT, bool kEnt>
+// This thread's sums over its windows of the part: first + tid, + NT, .... The usual d is one fma,
+// z c - mc with mc = m c rounded: every d is off by mc's rounding, which the end takes out again.
+// Where mc overflows (the lowest finite values, or an infinity) d is (z - m) c.
+//
+// ex2 runs at 16 a clock and SM, which leaves 8 of the 11 issue slots that HBM's rate allows an
+// element of bf16: the rest is therefore done on packed values (maximum, cut) and on pairs of fp32.
+// Without the pairs the entropy form took 406 us instead of the 352 us of the plain one (T=8192,
+// V=131072, bf16).
+template <int DT, int NT, bool kEnt>
 __device__ __forceinline__ RowSums thread_sums(const typename Elem<DT>::raw* row, const RowPart& p,
                                                float c) {
   using E = Elem<DT>;
   constexpr int VE = E::kVec;
   RowSums r{-INFINITY, 0.f, 0.f};
+  F2 s2 = f2(0.f), u2 = f2(0.f);
   float mc = 0.f;
-  for (int s0 = p.first + threadIdx.x; s0 < p.last; s0 += kLgThreads * kLgUnroll) {
+  const F2 c2 = f2(c);
+  const bool cut = cut_ok<DT>(c);
+  for (int s0 = p.first + threadIdx.x; s0 < p.last; s0 += NT * kLgUnroll) {
     uint4 w[kLgUnroll];
 #pragma unroll
     for (int j = 0; j < kLgUnroll; ++j) {
-      const int s = s0 + j * kLgThreads;
+      const int s = s0 + j * NT;
       // past the part: a window of an empty row, all -infinity
       w[j] = load_window<DT>(row, s < p.last ? p.n : 0, p.off, s);
     }
-    float tm = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < kLgUnroll; ++j) {
-      float x[VE];
-      E::unpack(w[j], x);
-#pragma unroll
-      for (int q = 0; q < VE; ++q) tm = fmaxf(tm, x[q]);
-    }
+    const float tm = E::max_of(w);
     if (tm > r.m) {
       const float mcn = __fmul_rn(tm, c);
       float d = shift_of(r.m, tm, c);
       if (r.m != -INFINITY && small_mc(mc) && small_mc(mcn)) d = fmaxf(mc - mcn, -1000.0f);
-      const float f = ex2(d);
-      if constexpr (kEnt) r.u = f * fmaf(d, r.s, r.u);
-      r.s *= f;
+      const F2 f = f2(ex2(d));
+      if constexpr (kEnt) u2 = f * fma2(f2(d), s2, u2);
+      s2 = f * s2;
       r.m = tm;
       mc = mcn;
     }
-    const bool usual = small_mc(mc);
+    if (small_mc(mc) && (!kEnt || cut)) {
+      const F2 nmc = f2(-mc);
 #pragma unroll
-    for (int j = 0; j < kLgUnroll; ++j) {
-      float x[VE];
-      E::unpack(w[j], x);
-      float ts = 0.f, tu = 0.f;
+      for (int j = 0; j < kLgUnroll; ++j) {
+        float x[VE];
+        E::unpack(kEnt ? E::cut(w[j]) : w[j], x);
 #pragma unroll
-      for (int q = 0; q < VE; ++q) {
-        const float d = usual ? fmaf(x[q], c, -mc) : (x[q] - r.m) * c;
-        const float e = ex2(d);
-        ts += e;
-        if constexpr (kEnt) tu = fmaf(e, fmaxf(d, kDCut), tu);
+        for (int q = 0; q < VE; q += 2) {
+          const F2 d = fma2(f2(x[q], x[q + 1]), c2, nmc);
+          const F2 e = ex2(d);
+          s2 = s2 + e;
+          if constexpr (kEnt) u2 = fma2(e, E::kCuts ? d : max2(d, kDCut), u2);
+        }
       }
-      r.s += ts;
-      if constexpr (kEnt) r.u += tu;
+    } else {
+      const bool usual = small_mc(mc);
+#pragma unroll
+      for (int j = 0; j < kLgUnroll; ++j) {
+        float x[VE];
+        E::unpack(w[j], x);
+#pragma unroll
+        for (int q = 0; q < VE; q += 2) {
+          F2 d;
+          if (usual)
+            d = fma2(f2(x[q], x[q + 1]), c2, f2(-mc));
+          else
+            d = f2((x[q] - r.m) * c, (x[q + 1] - r.m) * c);
+          const F2 e = ex2(d);
+          s2 = s2 + e;
+          if constexpr (kEnt) u2 = fma2(e, max2(d, kDCut), u2);
+        }
+      }
     }
   }
+  const float2 vs = split(s2), vu = split(u2);
+  r.s = vs.x + vs.y;
+  r.u = vu.x + vu.y;
   if (small_mc(mc)) {  // from the rounded mc to m c itself
     const float d = -fmaf(r.m, c, -mc), f = r.m == -INFINITY ? 1.0f : ex2(d);
     if constexpr (kEnt)
@@ -142,15 +176,15 @@ __device__ __forceinline__ RowSums rebase(RowSums r, float m, float c) {
 }
 
 // The sums of the whole part from its threads', in every thread.
-template <bool kEnt>
+template <int NT, bool kEnt>
 __device__ __forceinline__ RowSums block_sums(RowSums r, float c, float* red) {
-  const float m = block_max<kLgThreads>(r.m, red);
+  const float m = block_max<NT>(r.m, red);
   r = rebase<kEnt>(r, m, c);
   if constexpr (kEnt) {
-    const float2 v = block_sum2<kLgThreads>(r.s, r.u, red);
+    const float2 v = block_sum2<NT>(r.s, r.u, red);
     return {m, v.x, v.y};
   }
-  return {m, block_sum<kLgThreads>(r.s, red), 0.f};
+  return {m, block_sum<NT>(r.s, red), 0.f};
 }
 
 // The row's sums from the parts' (in shared memory of every CTA of the cluster), in rank order.
@@ -194,77 +228,91 @@ __device__ __forceinline__ unsigned long long top_key(uint32_t order, int index)
   return (static_cast<unsigned long long>(order) << 32) | (0xffffffffu - static_cast<uint32_t>(index));
 }
 
+template <int NT>
 struct TopShared {
-  unsigned long long cand[kLgCand];
+  // candidates; at least what the CTAs of a cluster join
+  static constexpr int kCand = 4 * NT > 8 * kLgTopMax ? 4 * NT : 8 * kLgTopMax;
+  unsigned long long cand[kCand];
   unsigned long long list[kLgTopMax];
-  unsigned long long warp_best[kLgThreads / 32];
-  uint32_t key[kLgThreads];
+  unsigned long long warp_best[NT / 32];
+  uint32_t key[NT];
+  int holder[NT];
   uint32_t threshold;
-  int count;
-  int scan[kLgThreads / 32];
+  int count, holders;
+  int scan[NT / 32];
 };
 
 // list[r] = the r-th largest of cand[0 .. n), r < K (the rest of the list stays as it is).
-__device__ __forceinline__ void rank_select(TopShared& sh, int n, int K) {
-  for (int i = threadIdx.x; i < n; i += kLgThreads) {
+template <int NT>
+__device__ __forceinline__ void rank_select(TopShared<NT>& sh, int n, int K) {
+  for (int i = threadIdx.x; i < n; i += NT) {
     const unsigned long long k = sh.cand[i];
     int r = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) r += sh.cand[j] > k;
     if (r < K && k != 0) sh.list[r] = k;
   }
 }
 
-// Adds this thread's elements with keys above `bar` (or at it, unless `above`) to the candidates.
-template <int DT>
+// Adds the elements with keys above `bar` (or at it, unless `above`) to the candidates. Only the
+// threads with a maximum that qualifies can hold such an element: their numbers are gathered, and
+// the whole CTA walks their windows, several at a time.
+template <int DT, int NT>
 __device__ __forceinline__ void collect(const typename Elem<DT>::raw* row, const RowPart& p,
-                                        uint32_t own, uint32_t bar, bool above, TopShared& sh) {
+                                        uint32_t own, uint32_t bar, bool above, TopShared<NT>& sh) {
   using E = Elem<DT>;
-  if (own == 0 || own < bar || (above && own == bar)) return;
-  for (int s0 = p.first + threadIdx.x; s0 < p.last; s0 += kLgThreads * kLgUnroll) {
+  const uint32_t least = above ? bar + 1 : bar > 0 ? bar : 1;  // keys stay below 2^32 - 1
+  if (own >= least) sh.holder[atomicAdd(&sh.holders, 1)] = threadIdx.x;
+  __syncthreads();
+  const int holders = sh.holders, per = (p.last - p.first + NT - 1) / NT;
+  for (int i0 = threadIdx.x; i0 < holders * per; i0 += NT * kLgUnroll) {
     uint4 w[kLgUnroll];
+    int at[kLgUnroll];
 #pragma unroll
     for (int j = 0; j < kLgUnroll; ++j) {
-      const int s = s0 + j * kLgThreads;
-      w[j] = load_window<DT>(row, s < p.last ? p.n : 0, p.off, s);
+      const int i = i0 + j * NT, h = i / per;
+      at[j] = i < holders * per ? p.first + sh.holder[h] + (i - h * per) * NT : p.last;
+      w[j] = load_window<DT>(row, at[j] < p.last ? p.n : 0, p.off, at[j]);
     }
 #pragma unroll
     for (int j = 0; j < kLgUnroll; ++j) {
-      const int s = s0 + j * kLgThreads;
-      if (s >= p.last) break;
+      if (at[j] >= p.last) continue;
       float x[E::kVec];
       E::unpack(w[j], x);
 #pragma unroll
       for (int q = 0; q < E::kVec; ++q) {
         const uint32_t k = order_key(x[q]);
-        const int e = window_first<DT>(s, p.off) + q;
-        if ((above ? k > bar : k >= bar) && e >= 0 && e < p.n) {
-          const int at = atomicAdd(&sh.count, 1);
-          if (at < kLgCand) sh.cand[at] = top_key(k, e);
+        const int e = window_first<DT>(at[j], p.off) + q;
+        if (k >= least && e >= 0 && e < p.n) {
+          const int to = atomicAdd(&sh.count, 1);
+          if (to < TopShared<NT>::kCand) sh.cand[to] = top_key(k, e);
         }
       }
     }
   }
+  __syncthreads();
 }
 
 // The part's K best into sh.list, in order. `m` is this thread's maximum.
 //
 // The K-th largest of the threads' maxima bounds the K-th largest element from below, and only
 // threads whose maximum reaches it can hold an element that does: for logits in no special order
-// about K threads walk their windows again, and a few more than K candidates are ranked. Where
-// more candidates than fit reach the bound, those above it are taken first and the missing ones
-// are the first elements equal to it (rows with long runs of one value: masked or constant rows);
-// where even those above it do not fit, K rounds each find the next best element.
-template <int DT>
+// about K threads' windows are walked again, and a few more than K candidates are ranked. Where
+// many more threads (rows with long runs of one value: masked or constant rows) or more candidates
+// than fit reach the bound, those above it are taken first and the missing ones are the first
+// elements equal to it; where even those above it do not fit, K rounds each find the next best
+// element.
+template <int DT, int NT>
 __device__ __forceinline__ void top_of_part(const typename Elem<DT>::raw* row, const RowPart& p,
-                                            float m, int K, TopShared& sh) {
+                                            float m, int K, TopShared<NT>& sh) {
   using E = Elem<DT>;
-  constexpr int NW = kLgThreads / 32;
+  constexpr int NW = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t own = p.first + tid < p.last ? order_key(m) : 0;
   __syncthreads();
   sh.key[tid] = own;
   if (tid < kLgTopMax) sh.list[tid] = 0;
-  if (tid == 0) sh.count = 0;
+  if (tid == 0) sh.count = 0, sh.holders = 0;
   __syncthreads();
   if (warp == 0) {
     uint32_t k[NW], prefix = 0;
@@ -275,7 +323,9 @@ __device__ __forceinline__ void top_of_part(const typename Elem<DT>::raw* row, c
       unsigned n = 0;
 #pragma unroll
       for (int i = 0; i < NW; ++i) n += k[i] >= trial;
-      if (__reduce_add_sync(0xffffffffu, n) >= static_cast<unsigned>(K)) prefix = trial;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (n >= static_cast<unsigned>(K)) prefix = trial;
+      if (n == static_cast<unsigned>(K)) break;
     }
     uint32_t lowest = 0xffffffffu;
 #pragma unroll
@@ -286,25 +336,25 @@ __device__ __forceinline__ void top_of_part(const typename Elem<DT>::raw* row, c
   }
   __syncthreads();
   const uint32_t bar = sh.threshold;  // 0 when fewer than K threads hold elements
-  collect<DT>(row, p, own, bar, false, sh);
-  __syncthreads();
-  int n = sh.count;
-  if (n <= kLgCand) {
-    rank_select(sh, n, K);
+  if (__syncthreads_count(own >= bar && own > 0) <= K + 32) {
+    collect<DT, NT>(row, p, own, bar, false, sh);
+    const int n = sh.count;
+    if (n <= TopShared<NT>::kCand) {
+      rank_select<NT>(sh, n, K);
+      __syncthreads();
+      return;
+    }
     __syncthreads();
-    return;
+    if (tid == 0) sh.count = 0, sh.holders = 0;
+    __syncthreads();
   }
-  __syncthreads();
-  if (tid == 0) sh.count = 0;
-  __syncthreads();
-  collect<DT>(row, p, own, bar, true, sh);
-  __syncthreads();
-  n = sh.count;
-  if (n <= kLgCand) {
-    rank_select(sh, n, K);
+  collect<DT, NT>(row, p, own, bar, true, sh);
+  const int n = sh.count;
+  if (n <= TopShared<NT>::kCand) {
+    rank_select<NT>(sh, n, K);
     // The first K - n elements equal to the bar, in index order.
     int found = n;
-    for (int base = p.first; base < p.last && found < K; base += kLgThreads) {
+    for (int base = p.first; base < p.last && found < K; base += NT) {
       const int s = base + tid;
       unsigned hits = 0;
       if (s < p.last) {
@@ -346,7 +396,7 @@ __device__ __forceinline__ void top_of_part(const typename Elem<DT>::raw* row, c
   for (int r = 0; r < K; ++r) {
     unsigned long long best = 0;
     if (own >= bar)
-      for (int s = p.first + tid; s < p.last; s += kLgThreads) {
+      for (int s = p.first + tid; s < p.last; s += NT) {
         float x[E::kVec];
         E::unpack(load_window<DT>(row, p.n, p.off, s), x);
 #pragma unroll
@@ -389,22 +439,22 @@ struct LogprobArgs {
 };
 
 // One cluster of `ranks` CTAs per row.
-template <int DT, bool kEnt, bool kTop>
-__global__ void __launch_bounds__(kLgThreads) logprob_kernel(const LogprobArgs a) {
+template <int DT, int NT, bool kEnt, bool kTop>
+__global__ void __launch_bounds__(NT) logprob_kernel(const LogprobArgs a) {
   using E = Elem<DT>;
-  __shared__ float red[2 * kLgThreads / 32];
+  __shared__ float red[2 * NT / 32];
   __shared__ RowSums part;
-  __shared__ typename std::conditional<kTop, TopShared, int>::type sh_top;
+  __shared__ typename std::conditional<kTop, TopShared<NT>, int>::type sh_top;
   pdl_wait();
   pdl_trigger();
   const int64_t t = blockIdx.x / a.ranks;
   const int rank = static_cast<int>(blockIdx.x - t * a.ranks);
   const auto* row = static_cast<const typename E::raw*>(a.logits) + t * a.stride;
   const RowPart p = row_part<DT>(row, a.V, rank, a.ranks);
-  const RowSums own = thread_sums<DT, kEnt>(row, p, a.c);
-  const RowSums mine = block_sums<kEnt>(own, a.c, red);
+  const RowSums own = thread_sums<DT, NT, kEnt>(row, p, a.c);
+  const RowSums mine = block_sums<NT, kEnt>(own, a.c, red);
   if (threadIdx.x == 0) part = mine;
-  if constexpr (kTop) top_of_part<DT>(row, p, own.m, a.K, sh_top);
+  if constexpr (kTop) top_of_part<DT, NT>(row, p, own.m, a.K, sh_top);
   __syncthreads();
   if (a.ranks > 1) cooperative_groups::this_cluster().sync();
   if (rank == 0) {
@@ -428,10 +478,10 @@ __global__ void __launch_bounds__(kLgThreads) logprob_kernel(const LogprobArgs a
       if (a.ranks > 1) {  // join the parts' lists
         auto cl = cooperative_groups::this_cluster();
         const int n = a.ranks * a.K;
-        for (int i = threadIdx.x; i < n; i += kLgThreads)
+        for (int i = threadIdx.x; i < n; i += NT)
           sh_top.cand[i] = cl.map_shared_rank(sh_top.list, i / a.K)[i % a.K];
         __syncthreads();
-        rank_select(sh_top, n, a.K);
+        rank_select<NT>(sh_top, n, a.K);
         __syncthreads();
       }
       const int k = threadIdx.x;
@@ -467,11 +517,11 @@ __device__ __forceinline__ float load_any(const void* p, int dtype, int64_t i) {
   return static_cast<const float*>(p)[i];
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kLgThreads) distill_kernel(const DistillArgs a) {
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a) {
   using E = Elem<DT>;
-  constexpr int PER = kLgTeacherMax / kLgThreads;
-  __shared__ float red[2 * kLgThreads / 32];
+  extern __shared__ float entries_f[];  // rank 0: [2][K]
+  __shared__ float red[2 * NT / 32];
   __shared__ RowSums part;
   pdl_wait();
   pdl_trigger();
@@ -479,51 +529,53 @@ __global__ void __launch_bounds__(kLgThreads) distill_kernel(const DistillArgs a
   const int rank = static_cast<int>(blockIdx.x - t * a.ranks);
   const auto* row = static_cast<const typename E::raw*>(a.logits) + t * a.stride;
   const RowPart p = row_part<DT>(row, a.V, rank, a.ranks);
-  const RowSums mine = block_sums<false>(thread_sums<DT, false>(row, p, a.c), a.c, red);
+  const RowSums mine = block_sums<NT, false>(thread_sums<DT, NT, false>(row, p, a.c), a.c, red);
   if (threadIdx.x == 0) part = mine;
   __syncthreads();
   if (a.ranks > 1) cooperative_groups::this_cluster().sync();
   if (rank == 0) {
     const RowSums r = cluster_sums<false>(&part, a.ranks, a.c);
     const float ls = logf(r.s);
-    // The teacher's softmax over its used entries.
-    float g[PER], tm = -INFINITY;
-    int id[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int k = threadIdx.x + i * kLgThreads;
-      const int64_t v = k < a.K ? a.index[t * a.K + k] : -1;
-      id[i] = v < 0 ? -1 : v >= a.V ? a.V : static_cast<int>(v);
-      g[i] = id[i] < 0 ? -INFINITY : load_any(a.teacher, a.teacher_dtype, t * a.K + k);
-      if (id[i] == a.V) g[i] = NAN;  // no such token: the row's loss and gradient say so
-      tm = fmaxf(tm, g[i]);
+    // The teacher's softmax over its used entries. Each thread keeps its entries' values in shared
+    // memory (scaled teacher logits; student logits).
+    float* gs = entries_f;
+    float* zs = gs + a.K;
+    float tm = -INFINITY;
+    for (int k = threadIdx.x; k < a.K; k += NT) {
+      const int64_t v = a.index[t * a.K + k];
+      float g = -INFINITY, z = 0.0f;
+      if (v >= a.V) {
+        g = NAN;  // no such token: the row's loss and gradient say so
+      } else if (v >= 0) {
+        g = load_any(a.teacher, a.teacher_dtype, t * a.K + k);
+        z = E::to_f32(row[v]);
+      }
+      gs[k] = g;
+      zs[k] = z;
+      tm = fmaxf(tm, g);
     }
-    tm = block_max<kLgThreads>(tm, red);
+    tm = block_max<NT>(tm, red);
     float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
+    for (int k = threadIdx.x; k < a.K; k += NT) {
       // tm = -infinity: nothing used; a NaN stays one
-      g[i] = tm == -INFINITY && !isnan(g[i]) ? -INFINITY : (g[i] - tm) * a.c;
-      sum += ex2(g[i]);
+      const float g = gs[k], d = tm == -INFINITY && !isnan(g) ? -INFINITY : (g - tm) * a.c;
+      gs[k] = d;
+      sum += ex2(d);
     }
-    sum = block_sum<kLgThreads>(sum, red);
+    sum = block_sum<NT>(sum, red);
     const float tl2 = log2f(sum);
     float loss = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int k = threadIdx.x + i * kLgThreads;
-      if (k >= a.K) continue;
-      const float w = sum == 0.0f || id[i] < 0 ? 0.0f : ex2(g[i]) / sum;
+    for (int k = threadIdx.x; k < a.K; k += NT) {
+      const float d = gs[k];
+      const bool unused = isnan(sum) && a.index[t * a.K + k] < 0;  // else d = -infinity says so
+      const float w = sum == 0.0f || unused ? 0.0f : ex2(d) / sum;
       a.weights[t * a.K + k] = w;
       if (w != 0.0f) {
-        const float lp = id[i] == a.V ? NAN
-                         : r.s == 0.0f
-                             ? -INFINITY
-                             : (E::to_f32(row[id[i]]) - r.m) * a.inv_t - ls;
-        loss = fmaf(w, kLn2 * (g[i] - tl2) - lp, loss);
+        const float lp = r.s == 0.0f ? -INFINITY : (zs[k] - r.m) * a.inv_t - ls;
+        loss = fmaf(w, kLn2 * (d - tl2) - lp, loss);
       }
     }
-    loss = block_sum<kLgThreads>(loss, red);
+    loss = block_sum<NT>(loss, red);
     if (threadIdx.x == 0) {
       a.loss[t] = loss;
       *reinterpret_cast<float2*>(a.stats + 2 * t) = make_float2(isnan(r.s) ? NAN : r.m, r.s);
@@ -548,11 +600,8 @@ struct LogitGradArgs {
   const float* weights;    // [T][K]
   const float* d_loss;
   float c, inv_t;
-  int V, K, chunks;
+  int V, K, chunks, rounds;
 };
-
-constexpr int kLgRounds = 2;  // of kLgUnroll windows per thread and chunk
-constexpr int kLgChunk = kLgThreads * kLgUnroll * kLgRounds;  // windows
 
 template <int DT>
 __device__ __forceinline__ void store_window(typename Elem<DT>::raw* out, int n, int e0,
@@ -576,13 +625,14 @@ __device__ __forceinline__ uint4 load_window_rw(const typename Elem<DT>::raw* ro
   return load_window<DT>(row, n, off, s);
 }
 
-// One chunk of a row per CTA. kDistill: the dense term g p of every element, then the few teacher
-// entries of the chunk once more, each formed in fp32 from its logit (read before any store).
-template <int DT, bool kDistill, bool kEnt>
-__global__ void __launch_bounds__(kLgThreads) logit_grad_kernel(const LogitGradArgs a) {
+// One chunk of a row per CTA: `rounds` times kLgUnroll windows a thread, the first of which are read
+// before anything else. kDistill: the dense term g p of every element, then the few teacher entries
+// of the chunk once more, each formed in fp32 from its logit (read before any store).
+template <int DT, int NT, bool kDistill, bool kEnt>
+__global__ void __launch_bounds__(NT) logit_grad_kernel(const LogitGradArgs a) {
   using E = Elem<DT>;
   constexpr int VE = E::kVec;
-  constexpr int PER = kLgTeacherMax / kLgThreads;
+  extern __shared__ int entries[];  // kDistill: [K] positions in the chunk (or -1), weights, logits
   pdl_wait();
   pdl_trigger();
   const int64_t t = blockIdx.x / a.chunks;
@@ -592,72 +642,47 @@ __global__ void __launch_bounds__(kLgThreads) logit_grad_kernel(const LogitGradA
   const int n = a.V, off = window_offset<DT>(row);
   const bool aligned =
       ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
-  const int first = chunk * kLgChunk;
-  const int last = min(first + kLgChunk, window_count<DT>(off, n));
+  const int first = chunk * a.rounds * (NT * kLgUnroll);
+  const int last = min(first + a.rounds * (NT * kLgUnroll), window_count<DT>(off, n));
+  uint4 w[kLgUnroll];
+  auto fetch = [&](int s0) {
+#pragma unroll
+    for (int j = 0; j < kLgUnroll; ++j) {
+      const int s = s0 + j * NT;
+      if (s < last) w[j] = load_window_rw<DT>(row, n, off, s);
+    }
+  };
+  fetch(first + threadIdx.x);
+
   const float2 st = *reinterpret_cast<const float2*>(a.stats + 2 * t);
   const float m = st.x, mc = __fmul_rn(st.x, a.c), is = 1.0f / st.y;
-  const bool usual = small_mc(mc);
+  const bool usual = small_mc(mc) && (!kEnt || cut_ok<DT>(a.c));
   const float off_d = usual ? fmaf(m, a.c, -mc) : 0.0f;  // what every d of the loop is too large by
 
   float A, B = 0.f, at_target = 0.f;
   int target = -1;
   bool zero;
-  // Distillation: this chunk's teacher entries (position, logit, summed weight).
-  [[maybe_unused]] int pos[PER];
-  [[maybe_unused]] float ez[PER], ew[PER];
+  const int lo = window_first<DT>(first, off);  // of the chunk's first window
   if constexpr (kDistill) {
-    __shared__ int s_pos[kLgTeacherMax];
-    __shared__ float s_w[kLgTeacherMax];
-    __shared__ uint32_t s_seen[kLgChunk * VE / 32];
-    __shared__ int s_twice;
-    const int lo = window_first<DT>(first, off);  // of the chunk's first window
-    for (int i = threadIdx.x; i < kLgChunk * VE / 32; i += kLgThreads) s_seen[i] = 0;
-    if (threadIdx.x == 0) s_twice = 0;
+    float* ws = reinterpret_cast<float*>(entries + a.K);
+    float* zs = ws + a.K;
     bool any = false, nan = false;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int k = threadIdx.x + i * kLgThreads;
-      pos[i] = -1;
-      if (k < a.K) {
-        const int64_t v = a.index[t * a.K + k];
-        const float w = a.weights[t * a.K + k];
-        any |= w != 0.0f;
-        nan |= isnan(w);
-        int q = -1;
-        if (v >= 0 && v < n && w != 0.0f) {
-          const int r = static_cast<int>(v) - lo;
-          if (r >= 0 && r < (last - first) * VE) q = r;
-        }
-        s_pos[k] = q;
-        s_w[k] = w;
-        pos[i] = q;
-        ew[i] = w;
-        if (q >= 0) {
-          ez[i] = E::to_f32(row[lo + q]);
-          if (atomicOr(&s_seen[q >> 5], 1u << (q & 31)) & (1u << (q & 31))) s_twice = 1;
-        }
+    for (int k = threadIdx.x; k < a.K; k += NT) {
+      const int64_t v = a.index[t * a.K + k];
+      const float wk = a.weights[t * a.K + k];
+      any |= wk != 0.0f;
+      nan |= isnan(wk);
+      int at = -1;
+      if (v >= 0 && v < n && wk != 0.0f) {
+        const int r = static_cast<int>(v) - lo;
+        if (r >= 0 && r < (last - first) * VE) at = r;
       }
+      entries[k] = at;
+      ws[k] = wk;
+      if (at >= 0) zs[k] = E::to_f32(row[lo + at]);
     }
     any = __syncthreads_or(any);
     nan = __syncthreads_or(nan);
-    if (s_twice) {  // an index given twice: its first entry adds up the weights, in entry order
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int k = threadIdx.x + i * kLgThreads;
-        if (pos[i] < 0) continue;
-        float w = 0.f;
-        for (int j = 0; j < a.K; ++j) {
-          if (s_pos[j] != pos[i]) continue;
-          if (j < k) {
-            pos[i] = -1;
-            break;
-          }
-          w += s_w[j];
-        }
-        ew[i] = w;
-      }
-    }
     const float g = a.d_loss[t];
     zero = g == 0.0f || st.y == 0.0f || !any;
     at_target = g * a.inv_t;  // times each entry's weight
@@ -687,19 +712,13 @@ __global__ void __launch_bounds__(kLgThreads) logit_grad_kernel(const LogitGradA
   }
   // e and d as the loop forms them carry off_d: taken out of the row's constants instead.
   const float fa = ex2(-off_d) * fmaf(-B, off_d, A), fb = ex2(-off_d) * B;
+  const F2 c2 = f2(a.c), nmc = f2(-mc), fa2 = f2(fa), fb2 = f2(fb);
 
-  for (int s0 = first + threadIdx.x; s0 < last; s0 += kLgThreads * kLgUnroll) {
-    uint4 w[kLgUnroll];
-    if (!zero) {
-#pragma unroll
-      for (int j = 0; j < kLgUnroll; ++j) {
-        const int s = s0 + j * kLgThreads;
-        if (s < last) w[j] = load_window_rw<DT>(row, n, off, s);
-      }
-    }
+  for (int s0 = first + threadIdx.x; s0 < last; s0 += NT * kLgUnroll) {
+    if (s0 >= first + NT * kLgUnroll && !zero) fetch(s0);
 #pragma unroll
     for (int j = 0; j < kLgUnroll; ++j) {
-      const int s = s0 + j * kLgThreads;
+      const int s = s0 + j * NT;
       if (s >= last) break;
       const int e0 = window_first<DT>(s, off);
       float x[VE];
@@ -707,15 +726,21 @@ __global__ void __launch_bounds__(kLgThreads) logit_grad_kernel(const LogitGradA
 #pragma unroll
         for (int q = 0; q < VE; ++q) x[q] = 0.0f;
       } else {
-        E::unpack(w[j], x);
+        E::unpack(kEnt && usual ? E::cut(w[j]) : w[j], x);
 #pragma unroll
-        for (int q = 0; q < VE; ++q) {
-          const float d = usual ? fmaf(x[q], a.c, -mc) : (x[q] - m) * a.c;
-          const float e = ex2(d);
-          if constexpr (kEnt)
-            x[q] = e * fmaf(fb, fmaxf(d, kDCut), fa);
+        for (int q = 0; q < VE; q += 2) {
+          F2 d;
+          if (usual)
+            d = fma2(f2(x[q], x[q + 1]), c2, nmc);
           else
-            x[q] = e * fa;
+            d = f2((x[q] - m) * a.c, (x[q + 1] - m) * a.c);
+          F2 e = ex2(d);
+          if constexpr (kEnt)
+            e = e * fma2(fb2, E::kCuts && usual ? d : max2(d, kDCut), fa2);
+          else
+            e = e * fa2;
+          const float2 v = split(e);
+          x[q] = v.x, x[q + 1] = v.y;
         }
         if constexpr (!kDistill) {
           const int at = target - e0;
@@ -730,14 +755,24 @@ __global__ void __launch_bounds__(kLgThreads) logit_grad_kernel(const LogitGradA
     }
   }
   if constexpr (kDistill) {
-    if (!zero) {
-      __syncthreads();
-      const int lo = window_first<DT>(first, off);
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (pos[i] >= 0)
-          out[lo + pos[i]] =
-              E::from_f32(fmaf(ex2((ez[i] - m) * a.c), A, -at_target * ew[i]));
+    if (zero) return;
+    __syncthreads();
+    const float* ws = reinterpret_cast<const float*>(entries + a.K);
+    const float* zs = ws + a.K;
+    for (int k = threadIdx.x; k < a.K; k += NT) {
+      const int at = entries[k];
+      if (at < 0) continue;
+      // An index given twice: its first entry adds up the weights, in entry order.
+      float sum = 0.f;
+      bool is_first = true;
+#pragma unroll 4
+      for (int j = 0; j < a.K; ++j)
+        if (entries[j] == at) {
+          is_first = is_first && j >= k;
+          sum += ws[j];
+        }
+      if (is_first)
+        out[lo + at] = E::from_f32(fmaf(ex2((zs[k] - m) * a.c), A, -at_target * sum));
     }
   }
 }
@@ -746,22 +781,31 @@ __global__ void __launch_bounds__(kLgThreads) logit_grad_kernel(const LogitGradA
 
 namespace {
 
+// Threads of a CTA: about eight windows each for short rows, so that one warp, which needs no
+// barrier, does a row of 1000 16-bit logits.
+int row_threads(int V, int vec) {
+  const int windows = (V + vec - 1) / vec;
+  return windows <= 256 ? 32 : windows <= 2048 ? 128 : 256;
+}
+
 // CTAs per row: one while the rows alone fill the device; for few rows a cluster of up to eight
 // shares each (every CTA keeping at least one round of windows).
-int row_ranks(int64_t T, int V, int vec) {
+int row_ranks(int64_t T, int V, int vec, int threads) {
   const int64_t want = 2 * static_cast<int64_t>(device_sm_count());
   int r = 1;
   while (r < 8 && T * r < want &&
-         static_cast<int64_t>(V) / (2 * r) >= static_cast<int64_t>(vec) * kLgThreads)
+         static_cast<int64_t>(V) / (2 * r) >= static_cast<int64_t>(vec) * threads)
     r *= 2;
   return r;
 }
 
 template <typename A>
-int launch_rows(void (*kernel)(A), int64_t T, int ranks, cudaStream_t s, const A& a) {
+int launch_rows(void (*kernel)(A), int64_t grid, int threads, int ranks, size_t smem,
+                cudaStream_t s, const A& a) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(T * ranks));
-  cfg.blockDim = dim3(kLgThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -777,30 +821,59 @@ int launch_rows(void (*kernel)(A), int64_t T, int ranks, cudaStream_t s, const A
   return e == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
 }
 
+// f(threads as a constant).
+template <typename F>
+int by_threads(int threads, F&& f) {
+  using std::integral_constant;
+  return threads == 32    ? f(integral_constant<int, 32>{})
+         : threads == 128 ? f(integral_constant<int, 128>{})
+                          : f(integral_constant<int, 256>{});
+}
+
 template <int DT>
 int launch_logprob(LogprobArgs a, int64_t T, cudaStream_t s) {
-  a.ranks = row_ranks(T, a.V, Elem<DT>::kVec);
-  auto kernel = a.entropy ? (a.K > 0 ? logprob_kernel<DT, true, true> : logprob_kernel<DT, true, false>)
-                          : (a.K > 0 ? logprob_kernel<DT, false, true> : logprob_kernel<DT, false, false>);
-  return launch_rows(kernel, T, a.ranks, s, a);
+  const int threads = row_threads(a.V, Elem<DT>::kVec);
+  a.ranks = row_ranks(T, a.V, Elem<DT>::kVec, threads);
+  return by_threads(threads, [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    auto kernel = a.entropy ? (a.K > 0 ? logprob_kernel<DT, NT, true, true>
+                                       : logprob_kernel<DT, NT, true, false>)
+                            : (a.K > 0 ? logprob_kernel<DT, NT, false, true>
+                                       : logprob_kernel<DT, NT, false, false>);
+    return launch_rows(kernel, T * a.ranks, NT, a.ranks, 0, s, a);
+  });
 }
 
 template <int DT>
 int launch_distill(DistillArgs a, int64_t T, cudaStream_t s) {
-  a.ranks = row_ranks(T, a.V, Elem<DT>::kVec);
-  return launch_rows(distill_kernel<DT>, T, a.ranks, s, a);
+  const int threads = row_threads(a.V, Elem<DT>::kVec);
+  a.ranks = row_ranks(T, a.V, Elem<DT>::kVec, threads);
+  return by_threads(threads, [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    return launch_rows(distill_kernel<DT, NT>, T * a.ranks, NT, a.ranks,
+                       static_cast<size_t>(a.K) * 8, s, a);
+  });
 }
 
 template <int DT>
 int launch_logit_grad(LogitGradArgs a, int64_t T, bool distill, cudaStream_t s) {
   // Windows of a row at its worst alignment.
   const int windows = (a.V + 2 * Elem<DT>::kVec - 2) / Elem<DT>::kVec;
-  a.chunks = (windows + kLgChunk - 1) / kLgChunk;
+  const int threads = windows <= 1024 ? 64 : 256;
+  a.rounds = 2;
+  const int chunk = threads * kLgUnroll * a.rounds;
+  a.chunks = (windows + chunk - 1) / chunk;
   if (T * a.chunks > (int64_t(1) << 31) - 1) return MHC_ERR_INVALID_ARG;
-  auto kernel = distill ? logit_grad_kernel<DT, true, false>
-                : a.d_entropy ? logit_grad_kernel<DT, false, true>
-                              : logit_grad_kernel<DT, false, false>;
-  return launch_rows(kernel, T * a.chunks, 1, s, a);
+  auto launch = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    auto kernel = distill      ? logit_grad_kernel<DT, NT, true, false>
+                  : a.d_entropy ? logit_grad_kernel<DT, NT, false, true>
+                                : logit_grad_kernel<DT, NT, false, false>;
+    const size_t smem = distill ? static_cast<size_t>(a.K) * 12 : 0;
+    return launch_rows(kernel, T * a.chunks, NT, 1, smem, s, a);
+  };
+  return threads == 64 ? launch(std::integral_constant<int, 64>{})
+                       : launch(std::integral_constant<int, 256>{});
 }
 
 bool temperature_ok(float t) {

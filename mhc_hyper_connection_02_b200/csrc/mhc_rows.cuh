@@ -27,6 +27,24 @@ struct Elem<0> {  // bf16
       x[2 * q + 1] = bf16_hi((&w.x)[q]);
     }
   }
+  // Each value at least -2^100 (a NaN stays one): finite, and below anything whose exponential
+  // matters.
+  static constexpr bool kCuts = true;
+  static __device__ __forceinline__ uint4 cut(uint4 w) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"((&w.x)[q]) : "r"(0xf180f180u));
+    return w;
+  }
+  // The largest of the windows' values, NaN apart.
+  template <int N>
+  static __device__ __forceinline__ float max_of(const uint4 (&w)[N]) {
+    uint32_t m = w[0].x;
+#pragma unroll
+    for (int i = 1; i < 4 * N; ++i)
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"((&w[i / 4].x)[i % 4]));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
+  }
   static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
     return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                       pack_bf16x2(x[6], x[7]));
@@ -53,6 +71,18 @@ struct Elem<1> {  // fp16
       x[2 * q + 1] = f.y;
     }
   }
+  // -infinity and the lowest finite value are too near for a cut between them.
+  static constexpr bool kCuts = false;
+  static __device__ __forceinline__ uint4 cut(uint4 w) { return w; }
+  template <int N>
+  static __device__ __forceinline__ float max_of(const uint4 (&w)[N]) {
+    uint32_t m = w[0].x;
+#pragma unroll
+    for (int i = 1; i < 4 * N; ++i)
+      asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"((&w[i / 4].x)[i % 4]));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return fmaxf(f.x, f.y);
+  }
   static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
     uint4 w;
 #pragma unroll
@@ -74,6 +104,15 @@ struct Elem<2> {  // fp32
   static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[4]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) x[q] = __uint_as_float((&w.x)[q]);
+  }
+  static constexpr bool kCuts = false;
+  static __device__ __forceinline__ uint4 cut(uint4 w) { return w; }
+  template <int N>
+  static __device__ __forceinline__ float max_of(const uint4 (&w)[N]) {
+    float m = __uint_as_float(w[0].x);
+#pragma unroll
+    for (int i = 1; i < 4 * N; ++i) m = fmaxf(m, __uint_as_float((&w[i / 4].x)[i % 4]));
+    return m;
   }
   static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
