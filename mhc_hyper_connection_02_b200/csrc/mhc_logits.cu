@@ -600,7 +600,7 @@ struct LogitGradArgs {
   const float* weights;    // [T][K]
   const float* d_loss;
   float c, inv_t;
-  int V, K, chunks, rounds;
+  int V, K, chunks;
 };
 
 template <int DT>
@@ -625,155 +625,262 @@ __device__ __forceinline__ uint4 load_window_rw(const typename Elem<DT>::raw* ro
   return load_window<DT>(row, n, off, s);
 }
 
-// One chunk of a row per CTA: `rounds` times kLgUnroll windows a thread, the first of which are read
-// before anything else. kDistill: the dense term g p of every element, then the few teacher entries
-// of the chunk once more, each formed in fp32 from its logit (read before any store).
-template <int DT, int NT, bool kDistill, bool kEnt>
-__global__ void __launch_bounds__(NT) logit_grad_kernel(const LogitGradArgs a) {
+// The constants of a row's gradient: e (fb d + fa) with e = 2^d (kEnt; e fa otherwise).
+struct GradRow {
+  float c, m, mc, fa, fb;
+  bool usual;  // d by one fma
+};
+template <int DT, bool kEnt>
+__device__ __forceinline__ GradRow grad_row(float c, float m, float A, float B) {
+  GradRow g;
+  g.c = c, g.m = m, g.mc = __fmul_rn(m, c);
+  g.usual = small_mc(g.mc) && (!kEnt || cut_ok<DT>(c));
+  // What every d of the usual form is too large by (see thread_sums): taken out of the constants.
+  const float off = g.usual ? fmaf(m, c, -g.mc) : 0.0f;
+  g.fa = ex2(-off) * fmaf(-B, off, A);
+  g.fb = ex2(-off) * B;
+  return g;
+}
+
+// A window's gradients without the terms of single elements.
+template <int DT, bool kEnt, bool kUsual>
+__device__ __forceinline__ void grad_window(uint4 w, const GradRow& g, float (&x)[Elem<DT>::kVec]) {
   using E = Elem<DT>;
-  constexpr int VE = E::kVec;
-  extern __shared__ int entries[];  // kDistill: [K] positions in the chunk (or -1), weights, logits
-  pdl_wait();
-  pdl_trigger();
-  const int64_t t = blockIdx.x / a.chunks;
-  const int chunk = static_cast<int>(blockIdx.x - t * a.chunks);
-  const auto* row = static_cast<const typename E::raw*>(a.logits) + t * a.stride;
-  auto* out = static_cast<typename E::raw*>(a.d_logits) + t * a.d_stride;
-  const int n = a.V, off = window_offset<DT>(row);
-  const bool aligned =
-      ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
-  const int first = chunk * a.rounds * (NT * kLgUnroll);
-  const int last = min(first + a.rounds * (NT * kLgUnroll), window_count<DT>(off, n));
-  uint4 w[kLgUnroll];
-  auto fetch = [&](int s0) {
+  E::unpack(kEnt && kUsual ? E::cut(w) : w, x);
+#pragma unroll
+  for (int q = 0; q < E::kVec; q += 2) {
+    F2 d;
+    if constexpr (kUsual)
+      d = fma2(f2(x[q], x[q + 1]), f2(g.c), f2(-g.mc));
+    else
+      d = f2((x[q] - g.m) * g.c, (x[q + 1] - g.m) * g.c);
+    F2 e = ex2(d);
+    if constexpr (kEnt)
+      e = e * fma2(f2(g.fb), E::kCuts && kUsual ? d : max2(d, kDCut), f2(g.fa));
+    else
+      e = e * f2(g.fa);
+    const float2 v = split(e);
+    x[q] = v.x, x[q + 1] = v.y;
+  }
+}
+
+// A chunk of a row: kLgRounds times kLgUnroll windows a thread. Twice as many windows took 3 % longer
+// for wide rows (fewer, longer CTAs: their tail), half as many 4 to 9 % (a chunk's start).
+constexpr int kLgRounds = 2;
+// CTAs that an SM has to hold: 1536 threads, at 40 registers. The passes wait for memory, and with
+// 1024 threads of 64 registers the distillation's took 376 us, with 1280 339 us, with these 331 us
+// (T=4096, V=131072, bf16).
+constexpr int grad_ctas(int threads) { return threads > 32 ? 1536 / threads : 1; }
+template <int DT, int NT>
+struct GradChunk {
+  using raw = typename Elem<DT>::raw;
+  const raw* row;
+  raw* out;
+  int off, first, last;  // windows [first, last)
+  bool aligned;
+  __device__ __forceinline__ GradChunk(const LogitGradArgs& a, int64_t t, int chunk) {
+    row = static_cast<const raw*>(a.logits) + t * a.stride;
+    out = static_cast<raw*>(a.d_logits) + t * a.d_stride;
+    off = window_offset<DT>(row);
+    aligned = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+    constexpr int per = NT * kLgUnroll * kLgRounds;
+    first = chunk * per;
+    last = min(first + per, window_count<DT>(off, a.V));
+  }
+  __device__ __forceinline__ void fetch(int n, int s0, uint4 (&w)[kLgUnroll]) const {
 #pragma unroll
     for (int j = 0; j < kLgUnroll; ++j) {
       const int s = s0 + j * NT;
       if (s < last) w[j] = load_window_rw<DT>(row, n, off, s);
     }
-  };
-  fetch(first + threadIdx.x);
+  }
+  // f(window, its first element, the values to store) forms the gradients of each of the thread's
+  // windows, the first of which are in w.
+  template <bool kRead, typename F>
+  __device__ __forceinline__ void walk(int n, uint4 (&w)[kLgUnroll], F&& f) const {
+    for (int s0 = first + threadIdx.x; s0 < last;) {
+#pragma unroll
+      for (int j = 0; j < kLgUnroll; ++j) {
+        const int s = s0 + j * NT;
+        if (s >= last) break;
+        const int e0 = window_first<DT>(s, off);
+        float x[Elem<DT>::kVec];
+        f(w[j], e0, x);
+        store_window<DT>(out, n, e0, aligned, x);
+      }
+      s0 += NT * kLgUnroll;
+      if (kRead && s0 < last) fetch(n, s0, w);
+    }
+  }
+  __device__ __forceinline__ void fill(int n, uint4 (&w)[kLgUnroll], float v) const {
+    walk<false>(n, w, [&](const uint4&, int, float (&x)[Elem<DT>::kVec]) {
+#pragma unroll
+      for (int q = 0; q < Elem<DT>::kVec; ++q) x[q] = v;
+    });
+  }
+};
+
+// Gradient of log probability and entropy, a chunk per CTA. The first windows are read before
+// anything else.
+template <int DT, int NT, bool kEnt>
+__global__ void __launch_bounds__(NT, grad_ctas(NT)) logprob_grad_kernel(const LogitGradArgs a) {
+  constexpr int VE = Elem<DT>::kVec;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t t = blockIdx.x / a.chunks;
+  const GradChunk<DT, NT> ch(a, t, static_cast<int>(blockIdx.x - t * a.chunks));
+  uint4 w[kLgUnroll];
+  ch.fetch(a.V, ch.first + threadIdx.x, w);
 
   const float2 st = *reinterpret_cast<const float2*>(a.stats + 2 * t);
-  const float m = st.x, mc = __fmul_rn(st.x, a.c), is = 1.0f / st.y;
-  const bool usual = small_mc(mc) && (!kEnt || cut_ok<DT>(a.c));
-  const float off_d = usual ? fmaf(m, a.c, -mc) : 0.0f;  // what every d of the loop is too large by
-
-  float A, B = 0.f, at_target = 0.f;
-  int target = -1;
-  bool zero;
-  const int lo = window_first<DT>(first, off);  // of the chunk's first window
-  if constexpr (kDistill) {
-    float* ws = reinterpret_cast<float*>(entries + a.K);
-    float* zs = ws + a.K;
-    bool any = false, nan = false;
-    for (int k = threadIdx.x; k < a.K; k += NT) {
-      const int64_t v = a.index[t * a.K + k];
-      const float wk = a.weights[t * a.K + k];
-      any |= wk != 0.0f;
-      nan |= isnan(wk);
-      int at = -1;
-      if (v >= 0 && v < n && wk != 0.0f) {
-        const int r = static_cast<int>(v) - lo;
-        if (r >= 0 && r < (last - first) * VE) at = r;
-      }
-      entries[k] = at;
-      ws[k] = wk;
-      if (at >= 0) zs[k] = E::to_f32(row[lo + at]);
-    }
-    any = __syncthreads_or(any);
-    nan = __syncthreads_or(nan);
-    const float g = a.d_loss[t];
-    zero = g == 0.0f || st.y == 0.0f || !any;
-    at_target = g * a.inv_t;  // times each entry's weight
-    A = nan ? NAN : at_target * is;
-  } else {
-    float glp = a.d_logprob ? a.d_logprob[t] : 0.0f;
-    if (glp != 0.0f) {
-      const int64_t y = a.targets[t];
-      if (y < 0)
-        glp = 0.0f;
-      else if (y >= n)
-        glp = NAN;
-      else
-        target = static_cast<int>(y);
-    }
-    at_target = glp * a.inv_t;
-    A = -at_target * is;
-    zero = glp == 0.0f;
-    if constexpr (kEnt) {
-      const float gent = a.d_entropy[t];
-      const float k = a.inv_t * is * gent;
-      A -= k * (a.entropy[t] - kLn2 * log2f(st.y));
-      B = -k * kLn2;
-      zero = zero && gent == 0.0f;
-    }
-    zero = zero || st.y == 0.0f;
+  const float is = 1.0f / st.y;
+  float glp = a.d_logprob ? a.d_logprob[t] : 0.0f;
+  int target = -VE;
+  if (glp != 0.0f) {
+    const int64_t y = a.targets[t];
+    if (y < 0)
+      glp = 0.0f;
+    else if (y >= a.V)
+      glp = NAN;
+    else
+      target = static_cast<int>(y);
   }
-  // e and d as the loop forms them carry off_d: taken out of the row's constants instead.
-  const float fa = ex2(-off_d) * fmaf(-B, off_d, A), fb = ex2(-off_d) * B;
-  const F2 c2 = f2(a.c), nmc = f2(-mc), fa2 = f2(fa), fb2 = f2(fb);
-
-  for (int s0 = first + threadIdx.x; s0 < last; s0 += NT * kLgUnroll) {
-    if (s0 >= first + NT * kLgUnroll && !zero) fetch(s0);
-#pragma unroll
-    for (int j = 0; j < kLgUnroll; ++j) {
-      const int s = s0 + j * NT;
-      if (s >= last) break;
-      const int e0 = window_first<DT>(s, off);
-      float x[VE];
-      if (zero) {
-#pragma unroll
-        for (int q = 0; q < VE; ++q) x[q] = 0.0f;
-      } else {
-        E::unpack(kEnt && usual ? E::cut(w[j]) : w[j], x);
-#pragma unroll
-        for (int q = 0; q < VE; q += 2) {
-          F2 d;
-          if (usual)
-            d = fma2(f2(x[q], x[q + 1]), c2, nmc);
-          else
-            d = f2((x[q] - m) * a.c, (x[q + 1] - m) * a.c);
-          F2 e = ex2(d);
-          if constexpr (kEnt)
-            e = e * fma2(fb2, E::kCuts && usual ? d : max2(d, kDCut), fa2);
-          else
-            e = e * fa2;
-          const float2 v = split(e);
-          x[q] = v.x, x[q + 1] = v.y;
-        }
-        if constexpr (!kDistill) {
-          const int at = target - e0;
-          if (target >= 0 && at >= 0 && at < VE) {
-#pragma unroll
-            for (int q = 0; q < VE; ++q)
-              if (q == at) x[q] += at_target;
-          }
-        }
-      }
-      store_window<DT>(out, n, e0, aligned, x);
-    }
+  const float at_target = glp * a.inv_t;
+  float A = -at_target * is, B = 0.f;
+  bool zero = glp == 0.0f;
+  if constexpr (kEnt) {
+    const float gent = a.d_entropy[t];
+    const float k = a.inv_t * is * gent;
+    A -= k * (a.entropy[t] - kLn2 * log2f(st.y));
+    B = -k * kLn2;
+    zero = zero && gent == 0.0f;
   }
-  if constexpr (kDistill) {
-    if (zero) return;
+  if (zero || st.y == 0.0f) {
+    ch.fill(a.V, w, 0.0f);
+    return;
+  }
+  const GradRow g = grad_row<DT, kEnt>(a.c, st.x, A, B);
+  auto walk = [&](auto usual) {
+    ch.template walk<true>(a.V, w, [&](const uint4& v, int e0, float (&x)[VE]) {
+      grad_window<DT, kEnt, decltype(usual)::value>(v, g, x);
+      const int at = target - e0;
+      if (at >= 0 && at < VE) {
+#pragma unroll
+        for (int q = 0; q < VE; ++q)
+          if (q == at) x[q] += at_target;
+      }
+    });
+  };
+  if (g.usual)
+    walk(std::true_type{});
+  else
+    walk(std::false_type{});
+}
+
+// Gradient of the distillation loss, a chunk per CTA: the dense term g p of every element, then the
+// few teacher entries of the chunk once more, each formed in fp32 from its logit. The entries are
+// read along with the first windows and wait in registers, so that the dense walk need not wait for
+// them; where it takes the logits' place, only its first store does. Two entries of one token are
+// told by a bit per element of the chunk; only then are the entries compared (comparing them always
+// took a tenth of the pass).
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, grad_ctas(NT)) distill_grad_kernel(const LogitGradArgs a) {
+  using E = Elem<DT>;
+  constexpr int VE = E::kVec;
+  constexpr int kSeen = NT * kLgUnroll * kLgRounds * VE / 32;
+  static_assert(kSeen % NT == 0, "whole words a thread");
+  enum { kAny = 1, kNan = 2, kTwice = 4 };
+  extern __shared__ int pos[];  // [K] positions in the chunk (or -1), weights, logits
+  __shared__ uint32_t seen[kSeen];
+  __shared__ int flags;
+  float* const ws = reinterpret_cast<float*>(pos) + a.K;
+  float* const zs = ws + a.K;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  const int64_t t = blockIdx.x / a.chunks;
+  const GradChunk<DT, NT> ch(a, t, static_cast<int>(blockIdx.x - t * a.chunks));
+  uint4 w[kLgUnroll];
+  ch.fetch(a.V, ch.first + tid, w);
+  struct Entry {
+    int at;  // position in the chunk, or -1
+    float w, z;
+  };
+  auto read_entry = [&](int k) {
+    const int64_t v = a.index[t * a.K + k];
+    Entry e{-1, a.weights[t * a.K + k], 0.f};
+    if (v >= 0 && v < a.V && e.w != 0.0f) {
+      const int r = static_cast<int>(v) - window_first<DT>(ch.first, ch.off);
+      if (r >= 0 && r < (ch.last - ch.first) * VE) e.at = r, e.z = E::to_f32(ch.row[v]);
+    }
+    return e;
+  };
+  auto keep_entry = [&](int k, const Entry& e) {
+    pos[k] = e.at;
+    ws[k] = e.w;
+    zs[k] = e.z;
+    int f = (e.w != 0.0f ? kAny : 0) | (isnan(e.w) ? kNan : 0);
+    if (e.at >= 0) {
+      const uint32_t bit = 1u << (e.at & 31);
+      if (atomicOr(&seen[e.at >> 5], bit) & bit) f |= kTwice;
+    }
+    if (f) atomicOr(&flags, f);
+  };
+  Entry e{-1, 0.f, 0.f};
+  if (tid < a.K) e = read_entry(tid);
+#pragma unroll
+  for (int i = 0; i < kSeen / NT; ++i) seen[i * NT + tid] = 0;
+  if (tid == 0) flags = 0;
+  if (a.K > NT || ch.row == ch.out) {
     __syncthreads();
-    const float* ws = reinterpret_cast<const float*>(entries + a.K);
-    const float* zs = ws + a.K;
-    for (int k = threadIdx.x; k < a.K; k += NT) {
-      const int at = entries[k];
-      if (at < 0) continue;
-      // An index given twice: its first entry adds up the weights, in entry order.
-      float sum = 0.f;
-      bool is_first = true;
-#pragma unroll 4
+    for (int k = tid + NT; k < a.K; k += NT) keep_entry(k, read_entry(k));
+    if (tid < a.K) zs[tid] = e.z;
+    __syncthreads();  // the entries' logits are read
+  }
+
+  const float2 st = *reinterpret_cast<const float2*>(a.stats + 2 * t);
+  const float dl = a.d_loss[t];
+  const float at_entry = dl * a.inv_t;  // times each entry's weight
+  const float A = at_entry / st.y;
+  if (dl == 0.0f || st.y == 0.0f) {
+    ch.fill(a.V, w, 0.0f);
+    return;
+  }
+  const GradRow g = grad_row<DT, false>(a.c, st.x, A, 0.0f);
+  auto walk = [&](auto usual) {
+    ch.template walk<true>(a.V, w, [&](const uint4& v, int, float (&x)[VE]) {
+      grad_window<DT, false, decltype(usual)::value>(v, g, x);
+    });
+  };
+  if (g.usual)
+    walk(std::true_type{});
+  else
+    walk(std::false_type{});
+
+  __syncthreads();  // seen and flags are clear, the dense terms stored
+  if (tid < a.K) keep_entry(tid, e);
+  __syncthreads();
+  const int flag = flags;
+  if ((flag & kNan) || !(flag & kAny)) {  // a weight without a value; no teacher's distribution
+    ch.fill(a.V, w, (flag & kNan) ? NAN : 0.0f);
+    return;
+  }
+  auto* const out = ch.out + window_first<DT>(ch.first, ch.off);
+  for (int k = tid; k < a.K; k += NT) {
+    const int at = pos[k];
+    if (at < 0) continue;
+    float sum = ws[k];
+    bool is_first = true;
+    if (flag & kTwice) {  // the first entry of a token adds up the weights, in entry order
+      sum = 0.f;
       for (int j = 0; j < a.K; ++j)
-        if (entries[j] == at) {
+        if (pos[j] == at) {
           is_first = is_first && j >= k;
           sum += ws[j];
         }
-      if (is_first)
-        out[lo + at] = E::from_f32(fmaf(ex2((zs[k] - m) * a.c), A, -at_target * sum));
     }
+    if (is_first)
+      out[at] = E::from_f32(fmaf(ex2((zs[k] - st.x) * a.c), A, -at_entry * sum));
   }
 }
 
@@ -799,9 +906,9 @@ int row_ranks(int64_t T, int V, int vec, int threads) {
   return r;
 }
 
-template <typename A>
-int launch_rows(void (*kernel)(A), int64_t grid, int threads, int ranks, size_t smem,
-                cudaStream_t s, const A& a) {
+template <typename... A>
+int launch_rows(void (*kernel)(A...), int64_t grid, int threads, int ranks, size_t smem,
+                cudaStream_t s, const A&... a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(threads);
@@ -816,7 +923,7 @@ int launch_rows(void (*kernel)(A), int64_t grid, int threads, int ranks, size_t 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ranks > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a...);
   note_launches(1);
   return e == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
 }
@@ -859,21 +966,18 @@ template <int DT>
 int launch_logit_grad(LogitGradArgs a, int64_t T, bool distill, cudaStream_t s) {
   // Windows of a row at its worst alignment.
   const int windows = (a.V + 2 * Elem<DT>::kVec - 2) / Elem<DT>::kVec;
-  const int threads = windows <= 1024 ? 64 : 256;
-  a.rounds = 2;
-  const int chunk = threads * kLgUnroll * a.rounds;
+  const int threads = windows <= 256 ? 32 : windows <= 1024 ? 128 : 256;
+  const int chunk = threads * kLgUnroll * kLgRounds;
   a.chunks = (windows + chunk - 1) / chunk;
-  if (T * a.chunks > (int64_t(1) << 31) - 1) return MHC_ERR_INVALID_ARG;
-  auto launch = [&](auto nt) {
+  const int64_t items = T * a.chunks;
+  if (items > (int64_t(1) << 31) - 1) return MHC_ERR_INVALID_ARG;
+  return by_threads(threads, [&](auto nt) {
     constexpr int NT = decltype(nt)::value;
-    auto kernel = distill      ? logit_grad_kernel<DT, NT, true, false>
-                  : a.d_entropy ? logit_grad_kernel<DT, NT, false, true>
-                                : logit_grad_kernel<DT, NT, false, false>;
-    const size_t smem = distill ? static_cast<size_t>(a.K) * 12 : 0;
-    return launch_rows(kernel, T * a.chunks, NT, 1, smem, s, a);
-  };
-  return threads == 64 ? launch(std::integral_constant<int, 64>{})
-                       : launch(std::integral_constant<int, 256>{});
+    auto kernel = distill       ? distill_grad_kernel<DT, NT>
+                  : a.d_entropy ? logprob_grad_kernel<DT, NT, true>
+                                : logprob_grad_kernel<DT, NT, false>;
+    return launch_rows(kernel, items, NT, 1, distill ? static_cast<size_t>(a.K) * 12 : 0, s, a);
+  });
 }
 
 bool temperature_ok(float t) {
