@@ -228,50 +228,49 @@ __global__ void __launch_bounds__(kWarp ? 32 * kNormWarpRows : K == 2 ? 512 : 10
   }
 }
 
-// Backward: d_x and the CTA's partial sums of the weights' gradients in one pass over x and d_y.
-// A CTA holds R groups of G threads (R = blockDim.x / G; kWarp: G = 32); group j of CTA i takes the
-// tokens i R + j, + gridDim.x R, ..., and reads the next token's rows before it works on this one's.
-// Each thread keeps its columns' gradient sums in registers; at the end the groups add theirs up
-// in order through shared memory.
-constexpr int norm_bwd_threads(int vw, int n, bool warp) {
-  return warp ? 256 : vw * n > 4 ? 512 : 1024;  // what the registers of 8 or 16 columns allow
+// to[c] = the sum of sums[j n + c] over the groups j, in order (n floats each).
+__device__ __forceinline__ void add_groups(const float* sums, int R, int n, float* to) {
+  for (int c = threadIdx.x; c < n; c += blockDim.x) {
+    float v = sums[c];
+    for (int j = 1; j < R; ++j) v += sums[static_cast<size_t>(j) * n + c];
+    to[c] = v;
+  }
 }
-template <int DT, int WT, int VW, int N, bool kWarp>
-__global__ void __launch_bounds__(norm_bwd_threads(VW, N, kWarp)) norm_bwd_row_kernel(const NormBwdArgs a,
-                                                                          int G) {
+
+// Backward for rows of any stride and alignment: d_x and the CTA's partial sums of the weights'
+// gradients in one pass over x and d_y, element by element. A CTA holds R groups of G threads; group
+// j of CTA i takes the tokens i R + j, + gridDim.x R, ..., and reads the next token's rows before it
+// exchanges sums for this one. Each thread keeps its N columns' gradient sums in registers; with one
+// column a thread (1024 threads a row) a row of 1001 took five times as long.
+template <int DT, int WT, int N>
+__global__ void __launch_bounds__(512) norm_bwd_row_kernel(const NormBwdArgs a, int G) {
   using W = Elem<WT>;
-  using C = Chunk<DT, VW>;
-  using raw = typename C::raw;
-  extern __shared__ float sums[];    // [2][H]: the groups' sums (R > 1)
-  __shared__ float red[2][64];  // by turn: each warp's two sums (sum_of_warps)
+  using E = Elem<DT>;
+  using raw = typename E::raw;
+  extern __shared__ float group_sums[];  // [R][2][H] (R > 1)
+  __shared__ float red[2][2 * 16];       // by turn: each warp's sums (joined_sums)
   pdl_wait();
   pdl_trigger();
-  if constexpr (kWarp) G = 32;
   const int R = blockDim.x / G;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5;
   const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
+  const int nw = G >> 5, w0 = group * nw;
   const auto* gamma = static_cast<const typename W::raw*>(a.gamma);
   const float fh = static_cast<float>(a.H);
-  float g[N][VW], dg[N][VW], db[N][VW];
+  float dg[N], db[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-#pragma unroll
-    for (int q = 0; q < VW; ++q) g[i][q] = 1.0f, dg[i][q] = 0.0f, db[i][q] = 0.0f;
-    const int h = (i * G + tid) * VW;
-    if (gamma && h < a.H) load_weights<WT, VW>(gamma + h, aligned32(gamma), g[i]);
-  }
+  for (int i = 0; i < N; ++i) dg[i] = db[i] = 0.0f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * R;
   int64_t t = blockIdx.x * static_cast<int64_t>(R) + group;
-  C cx[N], cd[N];
+  raw cx[N], cd[N];
   float mean = 0.f, rstd = 0.f;
   auto fetch = [&](int64_t at) {
+    const raw* x = static_cast<const raw*>(a.x) + at * a.x_stride;
+    const raw* dy = static_cast<const raw*>(a.dy) + at * a.dy_stride;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int h = (i * G + tid) * VW;
-      if (h < a.H) {
-        cx[i].load_ro(static_cast<const raw*>(a.x) + at * a.x_stride + h);
-        cd[i].load_ro(static_cast<const raw*>(a.dy) + at * a.dy_stride + h);
-      }
+      const int h = i * G + tid;
+      if (h < a.H) cx[i] = __ldg(x + h), cd[i] = __ldg(dy + h);
     }
     mean = a.mean[at];
     rstd = a.rstd[at];
@@ -279,93 +278,79 @@ __global__ void __launch_bounds__(norm_bwd_threads(VW, N, kWarp)) norm_bwd_row_k
   if (t < a.T) fetch(t);
   int turn = 0;
   for (; t < a.T; t += step, turn ^= 1) {
-    float xh[N][VW], q[N][VW], s1 = 0.f, s2 = 0.f;
+    float xh[N], q[N], sums[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if ((i * G + tid) * VW < a.H) {
-        cx[i].get(xh[i]);
-        cd[i].get(q[i]);
-#pragma unroll
-        for (int k = 0; k < VW; ++k) {
-          const float d = q[i][k];
-          xh[i][k] = (xh[i][k] - mean) * rstd;
-          dg[i][k] = fmaf(d, xh[i][k], dg[i][k]);
-          db[i][k] += d;
-          q[i][k] = d * g[i][k];
-          s1 += q[i][k];
-          s2 = fmaf(q[i][k], xh[i][k], s2);
-        }
+    for (int i = 0; i < N; ++i) {
+      const int h = i * G + tid;
+      if (h < a.H) {
+        const float d = E::to_f32(cd[i]);
+        xh[i] = (E::to_f32(cx[i]) - mean) * rstd;
+        dg[i] = fmaf(d, xh[i], dg[i]);
+        db[i] += d;
+        q[i] = gamma ? d * W::to_f32(__ldg(gamma + h)) : d;
+        sums[0] += q[i];
+        sums[1] = fmaf(q[i], xh[i], sums[1]);
       }
+    }
     const float r = rstd;
     if (t + step < a.T) fetch(t + step);
-    const float half = warp_sum_halves(s1, s2);
-    float2 p;
-    if constexpr (kWarp) {
-      p = join_halves(half);
+    const float part = warp_sums<2>(sums);
+    if (G == 32) {
+      share_sums<2>(part, sums);
     } else {
-      const int nw = G >> 5, w0 = group * nw;
-      if ((lane & 15) == 0) red[turn][2 * lane + warp] = half;
+      put_warp_sums<2>(part, red[turn], warp);
       asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(G) : "memory");
-      p = sum_of_warps(red[turn] + w0, nw);
+      joined_sums<2>(red[turn], w0, nw, sums);
     }
-    const float c1 = p.x / fh, c2 = p.y / fh;
+    const float c1 = sums[0] / fh, c2 = sums[1] / fh;
     raw* dx = static_cast<raw*>(a.dx) + t * a.H;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int h = (i * G + tid) * VW;
-      if (h < a.H) {
-#pragma unroll
-        for (int k = 0; k < VW; ++k) q[i][k] = r * (q[i][k] - c1 - xh[i][k] * c2);
-        C::put(dx + h, q[i]);
-      }
+      const int h = i * G + tid;
+      if (h < a.H) dx[h] = E::from_f32(r * (q[i] - c1 - xh[i] * c2));
     }
   }
   if (!a.part) return;
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
-  for (int j = 0; j < R; ++j) {
-    if (j > 0) __syncthreads();
-    if (group != j) continue;
-    float* out = j == R - 1 ? part : sums;
+  float* to = R > 1 ? group_sums + static_cast<size_t>(group) * 2 * a.H : part;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int h = (i * G + tid) * VW;
-      if (h < a.H) {
-#pragma unroll
-        for (int k = 0; k < VW; ++k) {
-          out[h + k] = j > 0 ? sums[h + k] + dg[i][k] : dg[i][k];
-          out[a.H + h + k] = j > 0 ? sums[a.H + h + k] + db[i][k] : db[i][k];
-        }
-      }
-    }
+  for (int i = 0; i < N; ++i) {
+    const int h = i * G + tid;
+    if (h < a.H) to[h] = dg[i], to[a.H + h] = db[i];
   }
+  if (R == 1) return;
+  __syncthreads();
+  add_groups(group_sums, R, 2 * a.H, part);
 }
 
-// Backward for wide rows (16-byte accesses): as above, but the tokens' rows of x and d_y are staged
-// in shared memory by 1-D bulk copies, several tokens ahead, and read from there twice instead of
-// being held in registers, which go to the columns' gradient sums. gamma is kept in shared memory
-// in fp32 (the first and the second four columns of each access apart, so that a warp's 16-byte
-// reads meet no bank twice). The last warp's first lane issues the copies; all waits are bounded,
-// and a group leaves its loop together (named_bar_or).
-template <int DT, int WT, int N>
-__global__ void __launch_bounds__(N == 4 ? 544 : 1024) norm_bwd_ring_kernel(const NormBwdArgs a, int G, int R,
-                                                             int stages) {
+// Backward for rows of 16-byte accesses. The tokens' rows of x and d_y are staged in shared memory
+// by 1-D bulk copies, K tokens to a stage; a group of G threads has S stages of its own and works
+// on one at a time. It reads the rows once (kHold: they stay packed in its registers) or twice, and
+// exchanges the sums of K tokens at once; the barrier of that exchange also tells its first thread
+// that a stage has been read and takes the next copy. Each thread keeps its columns' gradient sums
+// in registers over all its tokens: 16 columns at 512 threads an SM, which is what they and two held
+// rows leave room for. gamma is kept in shared memory in fp32, the first and the second four columns
+// of each access apart, so that a warp's 16-byte reads meet no bank twice. All waits are bounded,
+// and a group leaves its loop together.
+constexpr int kRingStages = 64;  // of all groups, at most
+template <int DT, int WT, int N, int K, bool kHold>
+__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a, int G, int R,
+                                                            int S) {
   using E = Elem<DT>;
   using W = Elem<WT>;
   using raw = typename E::raw;
-  constexpr int VW = E::kVec;
+  constexpr int VW = E::kVec, P = VW / 2;  // elements and pairs of an access
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ uint64_t full[8], empty[8];
-  __shared__ float red[2][64];  // by turn: each warp's two sums (sum_of_warps)
+  __shared__ uint64_t full[kRingStages];
+  __shared__ float red[2][2 * K * 16];  // by turn: each warp's sums (joined_sums)
   const int row_bytes = a.H * static_cast<int>(sizeof(raw));
-  float* gs = reinterpret_cast<float*>(ring + static_cast<size_t>(stages) * 2 * row_bytes);
+  const int stage_bytes = 2 * K * row_bytes;
+  float* gs = reinterpret_cast<float*>(ring + static_cast<size_t>(R * S) * stage_bytes);
   const int n = a.H / VW;  // accesses of a row
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5;
   const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < stages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], G / 32);
-    }
+    for (int i = 0; i < R * S; ++i) mbar_init(&full[i], 1);
     fence_mbarrier_init();
   }
   pdl_wait();
@@ -375,144 +360,192 @@ __global__ void __launch_bounds__(N == 4 ? 544 : 1024) norm_bwd_ring_kernel(cons
     gs[((h % VW) / 4 * n + h / VW) * 4 + h % 4] = gamma ? W::to_f32(gamma[h]) : 1.0f;
   __syncthreads();
 
-  if (group >= R) {
-    if (tid == 0) {
-      int64_t issued = 0;
-      bool ok = true;
-      for (int64_t t = blockIdx.x; t < a.T && ok; t += gridDim.x, ++issued) {
-        const int st = static_cast<int>(issued % stages);
-        if (issued >= stages)
-          ok = mbar_wait(&empty[st], static_cast<uint32_t>((issued / stages - 1) & 1), 130);
-        if (!ok) break;
-        uint8_t* to = ring + static_cast<size_t>(st) * 2 * row_bytes;
-        mbar_arrive_expect_tx(&full[st], 2u * row_bytes);
-        bulk_g2s(to, static_cast<const raw*>(a.x) + t * a.x_stride, row_bytes, &full[st]);
-        bulk_g2s(to + row_bytes, static_cast<const raw*>(a.dy) + t * a.dy_stride, row_bytes,
-                 &full[st]);
-      }
-      if (!ok)  // no copy into this CTA's shared memory may outlive it
-        for (int i = 0; i < stages; ++i) {
-          const int64_t k = issued / stages + (i < issued % stages ? 1 : 0);
-          if (k > 0) mbar_wait(&full[i], static_cast<uint32_t>((k - 1) & 1), 131);
-        }
+  // Group j of the CTA takes the tokens from ((i R + j) gridDim.x + blockIdx.x) K on, i = 0, 1, ....
+  const int64_t step = static_cast<int64_t>(gridDim.x) * K * R;
+  int64_t t = (static_cast<int64_t>(group) * gridDim.x + blockIdx.x) * K;
+  uint64_t* const mine = full + group * S;
+  uint8_t* const stages = ring + static_cast<size_t>(group * S) * stage_bytes;
+  auto copy = [&](int st, int64_t at) {  // by the group's first thread
+    uint8_t* to = stages + static_cast<size_t>(st) * stage_bytes;
+    const int rows = at + K <= a.T ? K : static_cast<int>(a.T - at);
+    mbar_arrive_expect_tx(&mine[st], 2u * rows * row_bytes);
+    for (int r = 0; r < rows; ++r, to += 2 * row_bytes) {
+      bulk_g2s(to, static_cast<const raw*>(a.x) + (at + r) * a.x_stride, row_bytes, &mine[st]);
+      bulk_g2s(to + row_bytes, static_cast<const raw*>(a.dy) + (at + r) * a.dy_stride, row_bytes,
+               &mine[st]);
     }
-    return;
-  }
-
+  };
+  if (tid == 0)
+    for (int i = 0; i < S && t + i * step < a.T; ++i) copy(i, t + i * step);
   const float fh = static_cast<float>(a.H);
-  constexpr int P = VW / 2;  // pairs of an access
   F2 dg[N][P], db[N][P];
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int q = 0; q < P; ++q) dg[i][q] = f2(0.0f), db[i][q] = f2(0.0f);
-  // The access at `at` of the staged rows, in pairs: x - mean, d_y and d_y gamma.
-  auto take = [&](const uint4* sx, const uint4* sd, int at, F2 neg_mean, F2 (&xm)[P], F2 (&d)[P],
-                  F2 (&v)[P]) {
-    float f[VW];
-    E::unpack(sx[at], f);
-#pragma unroll
-    for (int q = 0; q < P; ++q) xm[q] = f2(f[2 * q], f[2 * q + 1]) + neg_mean;
-    E::unpack(sd[at], f);
-#pragma unroll
-    for (int q = 0; q < P; ++q) d[q] = f2(f[2 * q], f[2 * q + 1]);
+  auto weights = [&](int at, F2 (&g)[P]) {
 #pragma unroll
     for (int q = 0; q < VW; q += 4) {
-      const float4 g = reinterpret_cast<const float4*>(gs)[q / 4 * n + at];
-      v[q / 2] = d[q / 2] * f2(g.x, g.y);
-      v[q / 2 + 1] = d[q / 2 + 1] * f2(g.z, g.w);
+      const float4 v = reinterpret_cast<const float4*>(gs)[q / 4 * n + at];
+      g[q / 2] = f2(v.x, v.y);
+      g[q / 2 + 1] = f2(v.z, v.w);
     }
   };
-  int64_t k = group;
-  int64_t t = blockIdx.x + k * static_cast<int64_t>(gridDim.x);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * R;
-  const int nw = G >> 5;
-  float mean = 0.f, rstd = 0.f;
-  if (t < a.T) mean = a.mean[t], rstd = a.rstd[t];
-  int turn = 0;
-  for (; t < a.T; t += step, k += R, turn ^= 1) {
-    const int st = static_cast<int>(k % stages);
-    const F2 neg_mean = f2(-mean);
-    const float r = rstd;
-    if (t + step < a.T) mean = a.mean[t + step], rstd = a.rstd[t + step];
-    const bool ok = mbar_wait(&full[st], static_cast<uint32_t>((k / stages) & 1), 132);
-    const uint4* sx = reinterpret_cast<const uint4*>(ring + static_cast<size_t>(st) * 2 * row_bytes);
-    const uint4* sd = sx + n;
-    F2 s1 = f2(0.f), s2 = f2(0.f);
+  auto pairs = [&](const uint4& w, F2 (&v)[P]) {
+    float f[VW];
+    E::unpack(w, f);
+#pragma unroll
+    for (int q = 0; q < P; ++q) v[q] = f2(f[2 * q], f[2 * q + 1]);
+  };
+  float mean[K], rstd[K];
+  auto stats = [&](int64_t t) {
+#pragma unroll
+    for (int r = 0; r < K; ++r)
+      if (t + r < a.T) mean[r] = a.mean[t + r], rstd[r] = a.rstd[t + r];
+  };
+  const int nw = G >> 5, w0 = group * nw;
+#pragma unroll
+  for (int r = 0; r < K; ++r) mean[r] = rstd[r] = 0.0f;
+  stats(t);
+  int st = 0, turn = 0;
+  uint32_t lap = 0;
+  bool ok = true;
+  for (; t < a.T; t += step, turn ^= 1) {
+    F2 nm[K], fr[K];
+    float rs[K];
+#pragma unroll
+    for (int r = 0; r < K; ++r) nm[r] = f2(-mean[r]), fr[r] = f2(rstd[r]), rs[r] = rstd[r];
+    const int rows = t + K <= a.T ? K : static_cast<int>(a.T - t);
+    ok = mbar_wait(&mine[st], lap & 1, 130);
+    const uint4* const sx =
+        reinterpret_cast<const uint4*>(stages + static_cast<size_t>(st) * stage_bytes);
+    uint4 hx[K][N], hd[K][N];
+    if constexpr (kHold) {
+#pragma unroll
+      for (int r = 0; r < K; ++r)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int at = i * G + tid;
+          if (at < n && r < rows) {
+            hx[r][i] = sx[2 * r * n + at];
+            hd[r][i] = sx[(2 * r + 1) * n + at];
+          } else {
+            hx[r][i] = hd[r][i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+    }
+    stats(t + step);
+    F2 s1[K], s2[K];
+#pragma unroll
+    for (int r = 0; r < K; ++r) s1[r] = s2[r] = f2(0.0f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int at = i * G + tid;
       if (at < n) {
-        F2 xm[P], d[P], v[P];
-        take(sx, sd, at, neg_mean, xm, d, v);
+        F2 g[P];
+        weights(at, g);
 #pragma unroll
-        for (int q = 0; q < P; ++q) {
-          const F2 xh = xm[q] * f2(r);
-          dg[i][q] = fma2(d[q], xh, dg[i][q]);
-          db[i][q] = db[i][q] + d[q];
-          s1 = s1 + v[q];
-          s2 = fma2(v[q], xh, s2);
+        for (int r = 0; r < K; ++r) {
+          F2 x[P], d[P];
+          pairs(kHold ? hx[r][i] : sx[2 * r * n + at], x);
+          pairs(kHold ? hd[r][i] : sx[(2 * r + 1) * n + at], d);
+#pragma unroll
+          for (int q = 0; q < P; ++q) {  // a row that is not there has d_y = 0
+            const F2 xh = (x[q] + nm[r]) * fr[r], v = d[q] * g[q];
+            dg[i][q] = fma2(d[q], xh, dg[i][q]);
+            db[i][q] = db[i][q] + d[q];
+            s1[r] = s1[r] + v;
+            s2[r] = fma2(v, xh, s2[r]);
+          }
         }
       }
     }
-    const float2 u1 = split(s1), u2 = split(s2);
-    const float half = warp_sum_halves(u1.x + u1.y, u2.x + u2.y);
-    if ((lane & 15) == 0) red[turn][2 * lane + warp] = half;
-    if (named_bar_or(group + 1, G, !ok)) break;
-    const float2 p = sum_of_warps(red[turn] + group * nw, nw);
+    float sums[2 * K];
+#pragma unroll
+    for (int r = 0; r < K; ++r) {
+      const float2 u1 = split(s1[r]), u2 = split(s2[r]);
+      sums[2 * r] = u1.x + u1.y;
+      sums[2 * r + 1] = u2.x + u2.y;
+    }
+    const float part = warp_sums<2 * K>(sums);
+    if (G == 32) {
+      ok = __all_sync(0xffffffffu, ok);
+      share_sums<2 * K>(part, sums);
+    } else {
+      put_warp_sums<2 * K>(part, red[turn], warp);
+      ok = !named_bar_or(group + 1, G, !ok);
+      joined_sums<2 * K>(red[turn], w0, nw, sums);
+    }
+    if (!ok) break;
+    // Every thread has read this stage (kHold), or the one before for the last time.
+    if (kHold) {
+      if (tid == 0 && t + S * step < a.T) copy(st, t + S * step);
+    } else {
+      if (tid == 0 && lap + st > 0 && t + (S - 1) * step < a.T)
+        copy(st > 0 ? st - 1 : S - 1, t + (S - 1) * step);
+    }
     // d_x = r v - r c1 - (x - mean) r^2 c2
-    const F2 fr = f2(r), f1 = f2(-r * (p.x / fh)), fx = f2(-r * r * (p.y / fh));
+    F2 f1[K], fx[K];
+#pragma unroll
+    for (int r = 0; r < K; ++r) {
+      f1[r] = f2(-rs[r] * (sums[2 * r] / fh));
+      fx[r] = f2(-rs[r] * rs[r] * (sums[2 * r + 1] / fh));
+    }
     raw* dx = static_cast<raw*>(a.dx) + t * a.H;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int at = i * G + tid;
       if (at < n) {
-        F2 xm[P], d[P], v[P];
-        take(sx, sd, at, neg_mean, xm, d, v);
-        float o[VW];
+        F2 g[P];
+        weights(at, g);
 #pragma unroll
-        for (int q = 0; q < P; ++q) {
-          const float2 u = split(fma2(v[q], fr, fma2(xm[q], fx, f1)));
-          o[2 * q] = u.x, o[2 * q + 1] = u.y;
+        for (int r = 0; r < K; ++r) {
+          if (r >= rows) break;
+          F2 x[P], d[P];
+          pairs(kHold ? hx[r][i] : sx[2 * r * n + at], x);
+          pairs(kHold ? hd[r][i] : sx[(2 * r + 1) * n + at], d);
+          float o[VW];
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            const float2 u = split(fma2(d[q] * g[q], fr[r], fma2(x[q] + nm[r], fx[r], f1[r])));
+            o[2 * q] = u.x, o[2 * q + 1] = u.y;
+          }
+          st_stream(dx + static_cast<int64_t>(r) * a.H + at * VW, E::pack(o));
         }
-        st_stream(dx + at * VW, E::pack(o));
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[st]);
+    if (++st == S) st = 0, ++lap;
+  }
+  if (!ok && tid == 0) {  // no copy into this CTA's shared memory may outlive it
+    const int ahead = kHold ? S : S - 1;  // stages with a copy from the current one on
+    for (int i = 0; i < S && t + i * step < a.T; ++i) {
+      if (i >= ahead && lap > 0) break;
+      mbar_wait(&mine[st], lap & 1, 131);
+      if (++st == S) st = 0, ++lap;
+    }
   }
   if (!a.part) return;
-  // The groups' sums, in order: through the stages' memory (free: every group is done), each
-  // access's first and second four columns apart as gamma's.
+  // The groups' sums, through the stages' memory (free: every group is done).
+  __syncthreads();
   float4* part = reinterpret_cast<float4*>(a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H);
-  float4* sums = reinterpret_cast<float4*>(ring);
-  for (int j = 0; j < R; ++j) {
-    if (R > 1) asm volatile("bar.sync 15, %0;" ::"r"(R * G) : "memory");
-    if (group != j) continue;
+  float4* to = R > 1 ? reinterpret_cast<float4*>(ring) + static_cast<size_t>(group) * (a.H / 2)
+                     : part;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = i * G + tid;
-      if (at < n) {
+  for (int i = 0; i < N; ++i) {
+    const int at = i * G + tid;
+    if (at < n) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
-#pragma unroll
-          for (int q = 0; q < P; q += 2) {
-            const float2 lo = split(w == 0 ? dg[i][q] : db[i][q]);
-            const float2 hi = split(w == 0 ? dg[i][q + 1] : db[i][q + 1]);
-            float4 v = make_float4(lo.x, lo.y, hi.x, hi.y);
-            float4* sum = sums + (w * (P / 2) + q / 2) * n + at;
-            if (j > 0) {
-              const float4 b = *sum;
-              v = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
-            }
-            if (j < R - 1)
-              *sum = v;
-            else
-              part[(w * a.H + at * VW) / 4 + q / 2] = v;
-          }
+      for (int q = 0; q < P; q += 2) {
+        const float2 lo = split(dg[i][q]), hi = split(dg[i][q + 1]);
+        to[at * (VW / 4) + q / 2] = make_float4(lo.x, lo.y, hi.x, hi.y);
+        const float2 lb = split(db[i][q]), hb = split(db[i][q + 1]);
+        to[a.H / 4 + at * (VW / 4) + q / 2] = make_float4(lb.x, lb.y, hb.x, hb.y);
       }
     }
   }
+  if (R == 1) return;
+  __syncthreads();
+  add_groups(reinterpret_cast<const float*>(ring), R, 2 * a.H, reinterpret_cast<float*>(part));
 }
 
 // ------------------------------------------------------------------------------ any row
@@ -607,37 +640,56 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_part_loop_kernel(const 
   p[a.H + h] = db;
 }
 
-// Adds `rows` partial rows of n = 2H floats in a fixed order: 8 warps of a block take every eighth
-// row of 32 columns, and the eight sums are added in order.
-__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* __restrict__ part, int rows,
-                                                           int64_t H, float* __restrict__ dgamma,
-                                                           float* __restrict__ dbeta) {
-  __shared__ float red[8][32];
+// Partial rows of the weights' gradients: enough CTAs to fill the device, and no more than tokens.
+// A device-independent bound keeps the workspace the same on every device.
+constexpr int kNormPartRows = 296;
+
+// Adds `rows` partial rows of n = 2H floats (V at a time) in a fixed order: thread (i, j) of a block
+// adds the rows j, j + 32, ... of its columns, all in flight at once, then the 32 sums are added in
+// order.
+constexpr int kSumLanes = 16, kSumRows = 32;
+template <int V>
+__global__ void __launch_bounds__(kSumLanes* kSumRows) norm_bwd_sum_kernel(
+    const float* __restrict__ part, int rows, int64_t H, float* __restrict__ dgamma,
+    float* __restrict__ dbeta) {
+  __shared__ float red[kSumRows][kSumLanes * V + 1];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t n = 2 * H, c = blockIdx.x * int64_t(32) + lane;
-  float s = 0.f;
-  if (c < n)
-    for (int r = warp; r < rows; r += 8) s += part[r * n + c];
-  red[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < n) {
+  const int i = threadIdx.x % kSumLanes, j = threadIdx.x / kSumLanes;
+  const int64_t n = 2 * H, base = blockIdx.x * static_cast<int64_t>(kSumLanes * V);
+  const int64_t c = base + i * V;
+  float s[V];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) s += red[w][lane];
-    if (c < H) {
-      if (dgamma) dgamma[c] = s;
+  for (int q = 0; q < V; ++q) s[q] = 0.0f;
+  if (c < n)
+#pragma unroll
+    for (int u = 0; u < (kNormPartRows + kSumRows - 1) / kSumRows; ++u) {
+      const int r = j + u * kSumRows;
+      if (r >= rows) break;
+      if constexpr (V == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(part + r * n + c);
+        s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
+      } else {
+        s[0] += part[r * n + c];
+      }
+    }
+#pragma unroll
+  for (int q = 0; q < V; ++q) red[j][i * V + q] = s[q];
+  __syncthreads();
+  const int64_t at = base + threadIdx.x;
+  if (threadIdx.x < kSumLanes * V && at < n) {
+    float v = red[0][threadIdx.x];
+#pragma unroll
+    for (int r = 1; r < kSumRows; ++r) v += red[r][threadIdx.x];
+    if (at < H) {
+      if (dgamma) dgamma[at] = v;
     } else if (dbeta) {
-      dbeta[c - H] = s;
+      dbeta[at - H] = v;
     }
   }
 }
 
 namespace {
-
-// Partial rows of the weights' gradients: enough CTAs to fill the device, and no more than tokens.
-// A device-independent bound keeps the workspace the same on every device.
-constexpr int kNormPartRows = 296;
 
 int norm_part_rows(int64_t T) { return static_cast<int>(T < kNormPartRows ? T : kNormPartRows); }
 
@@ -661,27 +713,29 @@ int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
 template <int DT, int WT, int VW>
 cudaError_t norm_forward_rows(const NormArgs& a, cudaStream_t s, bool* done) {
   const int64_t n = a.H / VW;  // accesses of a row (VW divides H)
+  constexpr int M = VW == 1 ? 16 : 4;  // of a thread, with many rows
   *done = true;
   const bool few = a.T < 2 * device_sm_count();
-  if (!few && n <= 256) {
+  if (!few && n <= 64 * M) {
     // A warp per row or two: no barrier.
-    auto k = n <= 32    ? norm_row_kernel<DT, WT, VW, 1, 2, true>
-             : n <= 64  ? norm_row_kernel<DT, WT, VW, 2, 2, true>
-             : n <= 128 ? norm_row_kernel<DT, WT, VW, 4, 2, true>
-                        : norm_row_kernel<DT, WT, VW, 8, 1, true>;
-    const int rows = kNormWarpRows * (n <= 128 ? 2 : 1);
+    auto k = n <= 32       ? norm_row_kernel<DT, WT, VW, 1, 2, true>
+             : n <= 64     ? norm_row_kernel<DT, WT, VW, 2, 2, true>
+             : n <= 32 * M ? norm_row_kernel<DT, WT, VW, M, 2, true>
+                           : norm_row_kernel<DT, WT, VW, 2 * M, 1, true>;
+    const int rows = kNormWarpRows * (n <= 32 * M ? 2 : 1);
     return launch_pdl(k, dim3(static_cast<unsigned>((a.T + rows - 1) / rows)),
                       dim3(32 * kNormWarpRows), 0, s, a);
   }
   // A CTA per two rows; with few rows one each, and as many threads as the row has work for.
-  const int per = few && n <= 1024 ? 1 : few && n <= 2048 ? 2 : 4;
+  const int per = few && n <= 1024 ? 1 : few && n <= 2048 ? 2 : M;
   const int G = round32((n + per - 1) / per);
   if (G <= 1024) {
+    const bool two = per == M && !few && G <= 512;
     auto k = per == 1   ? norm_row_kernel<DT, WT, VW, 1, 1, false>
              : per == 2 ? norm_row_kernel<DT, WT, VW, 2, 1, false>
-             : few || G > 512 ? norm_row_kernel<DT, WT, VW, 4, 1, false>
-                              : norm_row_kernel<DT, WT, VW, 4, 2, false>;
-    const int64_t grid = per < 4 || few || G > 512 ? a.T : (a.T + 1) / 2;
+             : two      ? norm_row_kernel<DT, WT, VW, M, 2, false>
+                        : norm_row_kernel<DT, WT, VW, M, 1, false>;
+    const int64_t grid = two ? (a.T + 1) / 2 : a.T;
     return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(G), 0, s, a);
   }
   *done = false;
@@ -703,64 +757,54 @@ int norm_forward(const NormArgs& a, cudaStream_t s) {
   return e == cudaSuccess ? 0 : MHC_ERR_CUDA;
 }
 
-// CTAs of a backward kernel: as many as are resident, no more than tokens or partial rows.
-unsigned norm_bwd_grid(const void* kernel, int threads, size_t smem, int64_t groups_of_tokens) {
-  int resident = 1;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, smem) !=
-          cudaSuccess ||
-      resident < 1)
-    resident = 1;
-  int64_t grid = static_cast<int64_t>(device_sm_count()) * resident;
-  if (grid > kNormPartRows) grid = kNormPartRows;
-  if (grid > groups_of_tokens) grid = groups_of_tokens;
-  return static_cast<unsigned>(grid);
+// CTAs of a backward kernel: one an SM (a device-independent bound keeps the workspace the same).
+unsigned norm_bwd_grid(int64_t most) {
+  const int64_t sms = device_sm_count() < kNormPartRows ? device_sm_count() : kNormPartRows;
+  return static_cast<unsigned>(most < sms ? most : sms);
 }
 
-// Launches the register form and returns its number of partial rows, or 0 (nothing launched) where
-// the row is too wide for it.
-template <int DT, int WT, int VW>
+// Launches the element-wise form and returns its number of partial rows, or 0 (nothing launched)
+// where the row is too wide for it.
+template <int DT, int WT>
 int norm_backward_rows(const NormBwdArgs& a, cudaStream_t s, cudaError_t* e) {
-  const int64_t n = a.H / VW;
-  const bool warp = n <= 64;
-  int per = 1;
-  while (per < 4 && (warp ? n > 32 * per : n > norm_bwd_threads(VW, per, false) * per)) per *= 2;
-  if (VW > 1 && per > 2) return 0;
-  const int G = warp ? 32 : round32((n + per - 1) / per);
-  if (G > norm_bwd_threads(VW, per, false)) return 0;
-  const int R = warp ? 8 : G >= 256 ? 1 : G >= 160 ? 2 : G >= 96 ? 4 : 8;
-  auto k = warp ? (per == 1 ? norm_bwd_row_kernel<DT, WT, VW, 1, true>
-                            : norm_bwd_row_kernel<DT, WT, VW, 2, true>)
-           : per == 1 ? norm_bwd_row_kernel<DT, WT, VW, 1, false>
-           : per == 2 ? norm_bwd_row_kernel<DT, WT, VW, 2, false>
-                      : norm_bwd_row_kernel<DT, WT, VW, (VW == 1 ? 4 : 1), false>;
-  const size_t smem = R > 1 ? static_cast<size_t>(2) * a.H * 4 : 0;
-  const unsigned grid =
-      norm_bwd_grid(reinterpret_cast<const void*>(k), G * R, smem, (a.T + R - 1) / R);
+  const int per = a.H <= 4096 ? 8 : 16;
+  const int G = round32((a.H + per - 1) / per);
+  if (G > 512) return 0;
+  const int R = G == 32 ? 16 : 512 / G < 15 ? 512 / G : 15;
+  const size_t smem = R > 1 ? static_cast<size_t>(R) * 2 * a.H * 4 : 0;
+  auto k = per == 8 ? norm_bwd_row_kernel<DT, WT, 8> : norm_bwd_row_kernel<DT, WT, 16>;
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(k), static_cast<int>(smem))) return 0;
+  const unsigned grid = norm_bwd_grid((a.T + R - 1) / R);
   *e = launch_pdl(k, dim3(grid), dim3(G * R), smem, s, a, G);
   note_launches(1);
   return static_cast<int>(grid);
 }
 
-// The staged form, likewise: rows of 16-byte accesses.
+// The staged form, likewise: rows of 16-byte accesses that fit twice beside gamma.
 template <int DT, int WT>
 int norm_backward_ring(const NormBwdArgs& a, cudaStream_t s, cudaError_t* e) {
-  const int64_t n = a.H / Elem<DT>::kVec;
-  if (n > 512 * 4) return 0;
-  const int per = n > 2 * 992 ? 4 : n > 330 ? 2 : 1;
+  constexpr int VW = Elem<DT>::kVec, N = 16 / VW;  // accesses of a thread that holds 16 columns
+  constexpr int K = VW == 8 ? 2 : 1;
+  const int64_t n = a.H / VW;
+  const bool hold = n <= 512 * N;
+  const int per = hold ? (n <= 32 ? 1 : N) : 2 * N;
   const int G = round32((n + per - 1) / per);
-  const int R = per == 4 || G > 496 ? 1 : G > 330 ? 2 : 3;
-  const size_t row = static_cast<size_t>(a.H) * sizeof(typename Elem<DT>::raw);
-  const size_t limit = 224 * 1024 - static_cast<size_t>(a.H) * 4;
-  const int stages = static_cast<int>(limit / (2 * row) < 8 ? limit / (2 * row) : 8);
-  if (stages < 2) return 0;
-  const size_t smem = stages * 2 * row + static_cast<size_t>(a.H) * 4;
-  auto k = per == 1   ? norm_bwd_ring_kernel<DT, WT, 1>
-           : per == 2 ? norm_bwd_ring_kernel<DT, WT, 2>
-                      : norm_bwd_ring_kernel<DT, WT, 4>;
+  if (G > 512) return 0;
+  const int R = G == 32 ? 16 : 512 / G < 15 ? 512 / G : 15;
+  const size_t stage = 2 * static_cast<size_t>(a.H) * sizeof(typename Elem<DT>::raw) * (hold ? K : 1);
+  const size_t weights = static_cast<size_t>(a.H) * 4, sums = R > 1 ? 2 * weights * R : 0;
+  const size_t fit = (224 * 1024 - weights) / (stage * R);
+  const int S = static_cast<int>(fit < kRingStages / 16 ? fit : kRingStages / 16);
+  if (S < 2) return 0;
+  // gamma lies behind the stages; the groups' sums may overwrite it
+  const size_t used = R * S * stage + weights, smem = used > sums ? used : sums;
+  auto k = !hold      ? norm_bwd_ring_kernel<DT, WT, 2 * N, 1, false>
+           : per == 1 ? norm_bwd_ring_kernel<DT, WT, 1, K, true>
+                      : norm_bwd_ring_kernel<DT, WT, N, K, true>;
   if (!ensure_smem_limit(reinterpret_cast<const void*>(k), static_cast<int>(smem))) return 0;
-  const unsigned grid =
-      norm_bwd_grid(reinterpret_cast<const void*>(k), G * R + 32, smem, a.T);
-  *e = launch_pdl(k, dim3(grid), dim3(G * R + 32), smem, s, a, G, R, stages);
+  const int rows = hold ? K : 1;
+  const unsigned grid = norm_bwd_grid((a.T + rows - 1) / rows);
+  *e = launch_pdl(k, dim3(grid), dim3(G * R), smem, s, a, G, R, S);
   note_launches(1);
   return static_cast<int>(grid);
 }
@@ -772,12 +816,9 @@ int norm_backward(NormBwdArgs a, float* dgamma, float* dbeta, cudaStream_t s) {
   if (!params) a.part = nullptr;
   cudaError_t e = cudaSuccess;
   int rows = 0;
-  if (vector_rows(VE, a.H, {a.x_stride, a.dy_stride}, {a.x, a.dy, a.dx, a.gamma})) {
-    if (a.H >= 2048) rows = norm_backward_ring<DT, WT>(a, s, &e);
-    if (rows == 0) rows = norm_backward_rows<DT, WT, VE>(a, s, &e);
-  } else {
-    rows = norm_backward_rows<DT, WT, 1>(a, s, &e);
-  }
+  if (vector_rows(VE, a.H, {a.x_stride, a.dy_stride}, {a.x, a.dy, a.dx, a.gamma}))
+    rows = norm_backward_ring<DT, WT>(a, s, &e);
+  if (rows == 0) rows = norm_backward_rows<DT, WT>(a, s, &e);
   if (rows == 0) {
     e = launch_pdl(norm_bwd_dx_loop_kernel<DT, WT>, dim3(row_grid(a.T)), dim3(kNormThreads), 0, s,
                    a);
@@ -793,9 +834,11 @@ int norm_backward(NormBwdArgs a, float* dgamma, float* dbeta, cudaStream_t s) {
   }
   if (e != cudaSuccess) return MHC_ERR_CUDA;
   if (!params) return 0;
-  e = launch_pdl(norm_bwd_sum_kernel, dim3(static_cast<unsigned>((2 * int64_t(a.H) + 31) / 32)),
-                 dim3(256), 0, s, static_cast<const float*>(a.part), rows, int64_t(a.H), dgamma,
-                 dbeta);
+  const int v = a.H % 2 == 0 ? 4 : 1;  // 2H floats are whole 16-byte accesses, and so is every row
+  e = launch_pdl(v == 4 ? norm_bwd_sum_kernel<4> : norm_bwd_sum_kernel<1>,
+                 dim3(static_cast<unsigned>((2 * int64_t(a.H) + kSumLanes * v - 1) / (kSumLanes * v))),
+                 dim3(kSumLanes * kSumRows), 0, s, static_cast<const float*>(a.part), rows,
+                 int64_t(a.H), dgamma, dbeta);
   note_launches(1);
   return e == cudaSuccess ? 0 : MHC_ERR_CUDA;
 }

@@ -243,6 +243,50 @@ __device__ __forceinline__ float2 sum_of_warps(const float* red, int nw) {
   return join_halves(v);
 }
 
+// The same for M = 2 or 4 sums of up to 16 warps: lanes j 32 / M to (j + 1) 32 / M hold sum j ...
+template <int M>
+__device__ __forceinline__ float warp_sums(const float (&v)[M]) {
+  if constexpr (M == 2) {
+    return warp_sum_halves(v[0], v[1]);
+  } else {
+    const bool high = (threadIdx.x & 16) != 0, odd = (threadIdx.x & 8) != 0;
+    float a = high ? v[2] : v[0], b = high ? v[3] : v[1];
+    a += __shfl_xor_sync(0xffffffffu, high ? v[0] : v[2], 16);
+    b += __shfl_xor_sync(0xffffffffu, high ? v[1] : v[3], 16);
+    float s = odd ? b : a;
+    s += __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  }
+}
+// ... which every lane gets all of,
+template <int M>
+__device__ __forceinline__ void share_sums(float s, float (&v)[M]) {
+#pragma unroll
+  for (int j = 0; j < M; ++j) v[j] = __shfl_sync(0xffffffffu, s, j * (32 / M));
+}
+// or which are put into red[16 M] ...
+template <int M>
+__device__ __forceinline__ void put_warp_sums(float s, float* red, int warp) {
+  const int lane = threadIdx.x & 31;
+  if (lane % (32 / M) == 0) red[lane / (32 / M) * 16 + warp] = s;
+}
+// and, after a barrier, joined over the warps w0 .. w0 + nw.
+template <int M>
+__device__ __forceinline__ void joined_sums(const float* red, int w0, int nw, float (&v)[M]) {
+  constexpr int L = 32 / M;
+  const int lane = threadIdx.x & 31, l = lane % L;
+  const float* r = red + lane / L * 16 + w0;
+  float s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; w += L)
+    if (l + w < nw) s += r[l + w];
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  share_sums<M>(s, v);
+}
+
 // Block reductions of NT threads: an xor tree in each warp, then the warps in order, the same bits
 // in every thread. `red` holds NT / 32 floats (2 NT / 32 for the pair); the leading barrier makes
 // it safe to use one array for several reductions.
