@@ -323,102 +323,438 @@ __global__ void __launch_bounds__(512) norm_bwd_row_kernel(const NormBwdArgs a, 
   add_groups(group_sums, R, 2 * a.H, part);
 }
 
-// Backward for rows of 16-byte accesses. The tokens' rows of x and d_y are staged in shared memory
-// by 1-D bulk copies, K tokens to a stage; a group of G threads has S stages of its own and works
-// on one at a time. It reads the rows once (kHold: they stay packed in its registers) or twice, and
-// exchanges the sums of K tokens at once; the barrier of that exchange also tells its first thread
-// that a stage has been read and takes the next copy. Each thread keeps its columns' gradient sums
-// in registers over all its tokens: 16 columns at 512 threads an SM, which is what they and two held
-// rows leave room for. gamma is kept in shared memory in fp32, the first and the second four columns
-// of each access apart, so that a warp's 16-byte reads meet no bank twice. All waits are bounded,
-// and a group leaves its loop together.
+// ------------------------------------------------------------------------------ staged rows
+//
+// Rows of one or two arrays (x; x and d_y) staged in shared memory by 1-D bulk copies, K tokens to a
+// stage; a group of G threads has S stages of its own and works on one at a time, and the barrier of
+// its exchange of sums also tells its first warp that a stage has been read and takes the next copy.
+//
+// Rows that are not whole 16-byte windows (odd widths, strides or addresses): where a row begins in
+// its first window (its phase) repeats every kVec tokens, so a CTA takes tokens of one class t mod
+// kVec only. Then every row of an array has the same phase there, columns stay with their threads,
+// and all accesses are whole windows. The output's phase sets the windows; an input of another phase
+// (a gap between its rows) is read as two windows and shifted. Bulk copies take the windows that the
+// row fills, single loads the up to kVec - 1 elements at either end.
+template <int DT, int A, int K, bool kAligned>
+struct RowRing {
+  using E = Elem<DT>;
+  using raw = typename E::raw;
+  static constexpr int VE = E::kVec;
+  const raw* base[A];
+  int64_t stride[A];
+  int off[A];         // phase of the class's rows
+  int shift[A];       // against the output's phase
+  // Tokens are below 2^31; a few stages beyond the last still fit 32 bits.
+  uint32_t T;            // tokens of the class
+  uint32_t first, step;  // in the class: the group's first, and from one stage to its next
+  int H, classes, cls;
+  int slot;           // windows of a row in a stage
+  uint8_t* stages;
+  uint64_t* full;
+  int S;
+
+  // Windows of a slot: those a row of n elements touches and, unaligned, one before and one after.
+  static __host__ __device__ __forceinline__ int slot_windows(int n) {
+    return kAligned ? n / VE : (n + 2 * VE - 2) / VE + 2;
+  }
+  __device__ __forceinline__ void init(int64_t tokens, int h, int C, int groups, int group,
+                                       int stages_each, uint8_t* memory, uint64_t* bars) {
+    classes = kAligned ? 1 : C;
+    cls = blockIdx.x % classes;
+    const int rank = blockIdx.x / classes, ranks = gridDim.x / classes;
+    T = static_cast<uint32_t>((tokens - cls + classes - 1) / classes);
+    first = (group * ranks + rank) * K;
+    step = ranks * K * groups;
+    H = h, S = stages_each;
+    slot = slot_windows(h);
+    stages = memory + static_cast<size_t>(group * S) * stage_bytes();
+    full = bars + group * S;
+  }
+  __device__ __forceinline__ void array(int i, const void* p, int64_t st, int out_off) {
+    base[i] = static_cast<const raw*>(p) + cls * st;
+    stride[i] = st * classes;
+    off[i] = kAligned ? 0 : window_offset<DT>(base[i]);
+    shift[i] = off[i] - out_off;
+  }
+  __device__ __forceinline__ int64_t token(uint32_t j) const {
+    return cls + static_cast<int64_t>(j) * classes;
+  }
+  __device__ __forceinline__ int stage_bytes() const { return A * K * slot * 16; }
+  __device__ __forceinline__ int rows(uint32_t j) const {
+    return j + K <= T ? K : static_cast<int>(T - j);
+  }
+  __device__ __forceinline__ uint4* slot_at(int st, int r, int i) const {
+    return reinterpret_cast<uint4*>(stages + static_cast<size_t>(st) * stage_bytes()) +
+           (r * A + i) * slot;
+  }
+
+  // The ends of a row: lane e of array i = lane / 16 takes one element, or none (-1).
+  __device__ __forceinline__ int edge(int lane) const {
+    const int o = A == 2 && lane >= 16 ? off[A - 1] : off[0], e = lane & 15;
+    if (A == 1 && lane >= 16) return -1;
+    if (e < 8) return o > 0 && e < VE - o ? e : -1;
+    const int at = (o + H) / VE * VE - o + e - 8;
+    return e - 8 < VE && at < H ? at : -1;
+  }
+  // Starts the copy of the tokens j .. into a stage (the group's first warp) and reads the ends of
+  // their rows, which put_edges writes there.
+  __device__ __forceinline__ void copy(int st, uint32_t j, int lane, raw (&ends)[K]) const {
+    const int n = rows(j);
+    if (lane == 0) {
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int i = 0; i < A; ++i)
+        bytes += kAligned ? H / VE : (off[i] + H) / VE - (off[i] > 0 ? 1 : 0);
+      mbar_arrive_expect_tx(&full[st], bytes * n * 16);
+      for (int r = 0; r < n; ++r)
+#pragma unroll
+        for (int i = 0; i < A; ++i) {
+          const int from = off[i] > 0 ? 1 : 0;  // the first window that the row fills
+          const raw* row = base[i] + static_cast<int64_t>(j + r) * stride[i];
+          bulk_g2s(slot_at(st, r, i) + (kAligned ? 0 : 1 + from),
+                   row + (from ? VE - off[i] : 0),
+                   ((kAligned ? 0 : off[i]) + H) / VE * 16 - from * 16, &full[st]);
+        }
+    }
+    if constexpr (!kAligned) {
+      const int at = edge(lane);
+      const bool second = A == 2 && lane >= 16;
+      const raw* from = second ? base[A - 1] : base[0];
+      const int64_t st_r = second ? stride[A - 1] : stride[0];
+#pragma unroll
+      for (int r = 0; r < K; ++r)
+        if (at >= 0 && r < n) ends[r] = from[static_cast<int64_t>(j + r) * st_r + at];
+    }
+  }
+  __device__ __forceinline__ void put_edges(int st, uint32_t j, int lane, const raw (&ends)[K]) const {
+    if constexpr (!kAligned) {
+      const int n = rows(j), at = edge(lane);
+      const bool second = A == 2 && lane >= 16;
+      const int o = second ? off[A - 1] : off[0];
+#pragma unroll
+      for (int r = 0; r < K; ++r)
+        if (at >= 0 && r < n)
+          reinterpret_cast<raw*>(slot_at(st, r, second ? 1 : 0) + 1)[o + at] = ends[r];
+    }
+  }
+
+  // Output window s of row r of array i; what lies outside the row comes back as zero.
+  __device__ __forceinline__ uint4 window(int st, int r, int i, int s, int out_off) const {
+    const uint4* p = slot_at(st, r, i) + s;
+    if constexpr (kAligned) {
+      return *p;
+    } else {
+      uint4 w;
+      if (shift[i] == 0) {
+        w = p[1];
+      } else {
+        const int by = (shift[i] & (VE - 1)) * static_cast<int>(sizeof(raw));  // bytes
+        if (shift[i] > 0) ++p;
+        const uint4 lo = p[0], hi = p[1];
+        uint32_t v[6] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y};
+        uint32_t u[5];
+        if (by & 8) {
+          v[0] = lo.z, v[1] = lo.w, v[2] = hi.x, v[3] = hi.y, v[4] = hi.z, v[5] = hi.w;
+        }
+#pragma unroll
+        for (int q = 0; q < 5; ++q) u[q] = (by & 4) ? v[q + 1] : v[q];
+        const int bits = (by & 3) * 8;
+        w = make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
+                       __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits));
+      }
+      const int e0 = s * VE - out_off;
+      if (e0 < 0 || e0 + VE > H) {
+        uint32_t* words = &w.x;
+#pragma unroll
+        for (int q = 0; q < VE; ++q)
+          if (e0 + q < 0 || e0 + q >= H) {
+            if constexpr (DT == 2)
+              words[q] = 0;
+            else
+              words[q / 2] &= q % 2 ? 0x0000ffffu : 0xffff0000u;
+          }
+      }
+      return w;
+    }
+  }
+
+  // After a wait that gave up in stage st: no copy into this CTA's shared memory may outlive it.
+  __device__ __forceinline__ void drain(int st, uint32_t lap, uint32_t j, int ahead) const {
+    for (int i = 0; i < ahead && j + i * step < T; ++i) {
+      mbar_wait(&full[st], lap & 1, 131);
+      if (++st == S) st = 0, ++lap;
+    }
+  }
+};
+
+// One weight per element of the windows, in fp32 (zero outside the row), the first and the second
+// four of each window apart, so that a warp's 16-byte reads meet no bank twice.
+template <int VE, typename W>
+__device__ __forceinline__ void stage_weights(float* to, const typename W::raw* w, float otherwise,
+                                              int H, int off, int n) {
+  for (int i = threadIdx.x; i < n * VE; i += blockDim.x) {
+    const int h = i - off;
+    to[((i % VE) / 4 * n + i / VE) * 4 + i % 4] =
+        h < 0 || h >= H ? 0.0f : w ? W::to_f32(w[h]) : otherwise;
+  }
+}
+template <int VE>
+__device__ __forceinline__ void staged_weights(const float* from, int n, int s, F2 (&g)[VE / 2]) {
+#pragma unroll
+  for (int q = 0; q < VE; q += 4) {
+    const float4 v = reinterpret_cast<const float4*>(from)[q / 4 * n + s];
+    g[q / 2] = f2(v.x, v.y);
+    g[q / 2 + 1] = f2(v.z, v.w);
+  }
+}
+template <int DT>
+__device__ __forceinline__ void unpack_pairs(const uint4& w, F2 (&v)[Elem<DT>::kVec / 2]) {
+  float f[Elem<DT>::kVec];
+  Elem<DT>::unpack(w, f);
+#pragma unroll
+  for (int q = 0; q < Elem<DT>::kVec / 2; ++q) v[q] = f2(f[2 * q], f[2 * q + 1]);
+}
+// Windows' output: whole ones at once, the elements of those at a row's ends one by one.
+template <int DT, bool kAligned>
+__device__ __forceinline__ void put_window(typename Elem<DT>::raw* row, int H, int e0,
+                                           const F2 (&v)[Elem<DT>::kVec / 2]) {
+  using E = Elem<DT>;
+  float o[E::kVec];
+#pragma unroll
+  for (int q = 0; q < E::kVec / 2; ++q) {
+    const float2 u = split(v[q]);
+    o[2 * q] = u.x, o[2 * q + 1] = u.y;
+  }
+  if (kAligned || (e0 >= 0 && e0 + E::kVec <= H)) {
+    st_stream(row + e0, E::pack(o));
+  } else {
+#pragma unroll
+    for (int q = 0; q < E::kVec; ++q)
+      if (e0 + q >= 0 && e0 + q < H) row[e0 + q] = E::from_f32(o[q]);
+  }
+}
+
 constexpr int kRingStages = 64;  // of all groups, at most
-template <int DT, int WT, int N, int K, bool kHold>
-__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a, int G, int R,
-                                                            int S) {
+
+// Forward of rows that are not whole windows. x is read once and stays packed in registers.
+template <int DT, int WT, int N, int K>
+__global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a, int G, int R, int S,
+                                                        int C) {
   using E = Elem<DT>;
   using W = Elem<WT>;
   using raw = typename E::raw;
-  constexpr int VW = E::kVec, P = VW / 2;  // elements and pairs of an access
+  constexpr int VE = E::kVec, P = VE / 2;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kRingStages];
-  __shared__ float red[2][2 * K * 16];  // by turn: each warp's sums (joined_sums)
-  const int row_bytes = a.H * static_cast<int>(sizeof(raw));
-  const int stage_bytes = 2 * K * row_bytes;
-  float* gs = reinterpret_cast<float*>(ring + static_cast<size_t>(R * S) * stage_bytes);
-  const int n = a.H / VW;  // accesses of a row
-  const int warp = threadIdx.x >> 5;
+  __shared__ float red[2][2 * 16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
   if (threadIdx.x == 0) {
     for (int i = 0; i < R * S; ++i) mbar_init(&full[i], 1);
     fence_mbarrier_init();
   }
+  RowRing<DT, 1, K, false> rr;
+  rr.init(a.T, a.H, C, R, group, S, ring, full);
+  raw* const y0 = static_cast<raw*>(a.y) + static_cast<int64_t>(rr.cls) * a.H;
+  const int off = window_offset<DT>(y0), n = window_count<DT>(off, a.H);
+  rr.array(0, a.x, a.x_stride, off);
+  float* const gs = reinterpret_cast<float*>(ring + static_cast<size_t>(R * S) * rr.stage_bytes());
+  float* const bs = gs + n * VE;
   pdl_wait();
   pdl_trigger();
-  const auto* gamma = static_cast<const typename W::raw*>(a.gamma);
-  for (int h = threadIdx.x; h < a.H; h += blockDim.x)
-    gs[((h % VW) / 4 * n + h / VW) * 4 + h % 4] = gamma ? W::to_f32(gamma[h]) : 1.0f;
+  stage_weights<VE, W>(gs, static_cast<const typename W::raw*>(a.gamma), 1.0f, a.H, off, n);
+  stage_weights<VE, W>(bs, static_cast<const typename W::raw*>(a.beta), 0.0f, a.H, off, n);
+  __syncthreads();
+  raw ends[K];
+  if (tid < 32)
+    for (int i = 0; i < S && rr.first + i * rr.step < rr.T; ++i) {
+      rr.copy(i, rr.first + i * rr.step, lane, ends);
+      rr.put_edges(i, rr.first + i * rr.step, lane, ends);
+    }
   __syncthreads();
 
-  // Group j of the CTA takes the tokens from ((i R + j) gridDim.x + blockIdx.x) K on, i = 0, 1, ....
-  const int64_t step = static_cast<int64_t>(gridDim.x) * K * R;
-  int64_t t = (static_cast<int64_t>(group) * gridDim.x + blockIdx.x) * K;
-  uint64_t* const mine = full + group * S;
-  uint8_t* const stages = ring + static_cast<size_t>(group * S) * stage_bytes;
-  auto copy = [&](int st, int64_t at) {  // by the group's first thread
-    uint8_t* to = stages + static_cast<size_t>(st) * stage_bytes;
-    const int rows = at + K <= a.T ? K : static_cast<int>(a.T - at);
-    mbar_arrive_expect_tx(&mine[st], 2u * rows * row_bytes);
-    for (int r = 0; r < rows; ++r, to += 2 * row_bytes) {
-      bulk_g2s(to, static_cast<const raw*>(a.x) + (at + r) * a.x_stride, row_bytes, &mine[st]);
-      bulk_g2s(to + row_bytes, static_cast<const raw*>(a.dy) + (at + r) * a.dy_stride, row_bytes,
-               &mine[st]);
+  const float fh = static_cast<float>(a.H);
+  const int nw = G >> 5, w0 = group * nw;
+  int turn = 0;
+  bool ok = true;
+  auto total = [&](const float (&v)[K], float (&out)[K]) {  // over the group, which agrees on ok
+    float sums[2] = {v[0], K == 2 ? v[K - 1] : 0.0f};
+    const float part = warp_sums<2>(sums);
+    if (G == 32) {
+      ok = __all_sync(0xffffffffu, ok);
+      share_sums<2>(part, sums);
+    } else {
+      put_warp_sums<2>(part, red[turn], warp);
+      ok = !named_bar_or(group + 1, G, !ok);
+      joined_sums<2>(red[turn], w0, nw, sums);
+      turn ^= 1;
     }
+    out[0] = sums[0];
+    if (K == 2) out[K - 1] = sums[1];
   };
-  if (tid == 0)
-    for (int i = 0; i < S && t + i * step < a.T; ++i) copy(i, t + i * step);
+  int st = 0;
+  uint32_t lap = 0;
+  uint32_t j = rr.first;
+  for (; j < rr.T; j += rr.step) {
+    const int rows = rr.rows(j);
+    ok = mbar_wait(&rr.full[st], lap & 1, 132);
+    uint4 h[K][N];
+    float s[K], mean[K], v[K], rstd[K];
+#pragma unroll
+    for (int r = 0; r < K; ++r) {
+      F2 sum = f2(0.0f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int at = i * G + tid;
+        h[r][i] = at < n && r < rows ? rr.window(st, r, 0, at, off) : make_uint4(0, 0, 0, 0);
+        F2 x[P];
+        unpack_pairs<DT>(h[r][i], x);
+#pragma unroll
+        for (int q = 0; q < P; ++q) sum = sum + x[q];
+      }
+      const float2 u = split(sum);
+      s[r] = u.x + u.y;
+    }
+    total(s, mean);
+    if (!ok) break;
+    const bool more = j + S * rr.step < rr.T;
+    if (G == 32) __syncwarp();
+    if (tid < 32 && more) rr.copy(st, j + S * rr.step, lane, ends);
+#pragma unroll
+    for (int r = 0; r < K; ++r) {
+      mean[r] /= fh;
+      F2 sum = f2(0.0f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int at = i * G + tid, e0 = at * VE - off;
+        if (at < n) {
+          F2 x[P];
+          unpack_pairs<DT>(h[r][i], x);
+          if (e0 >= 0 && e0 + VE <= a.H) {
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+              const F2 d = x[q] + f2(-mean[r]);
+              sum = fma2(d, d, sum);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+              const float2 u = split(x[q]);
+              const int e = e0 + 2 * q;
+              const F2 d = f2(e >= 0 && e < a.H ? u.x - mean[r] : 0.0f,
+                              e + 1 >= 0 && e + 1 < a.H ? u.y - mean[r] : 0.0f);
+              sum = fma2(d, d, sum);
+            }
+          }
+        }
+      }
+      const float2 u = split(sum);
+      v[r] = u.x + u.y;
+    }
+    total(v, rstd);
+#pragma unroll
+    for (int r = 0; r < K; ++r) {
+      rstd[r] = 1.0f / sqrtf(rstd[r] / fh + a.eps);
+      if (tid == 0 && r < rows) {
+        const int64_t t = rr.token(j + r);
+        if (a.mean) a.mean[t] = mean[r];
+        if (a.rstd) a.rstd[t] = rstd[r];
+      }
+    }
+    raw* const y = y0 + static_cast<int64_t>(j) * rr.classes * a.H;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = i * G + tid;
+      if (at < n) {
+        F2 g[P], b[P];
+        staged_weights<VE>(gs, n, at, g);
+        staged_weights<VE>(bs, n, at, b);
+#pragma unroll
+        for (int r = 0; r < K; ++r) {
+          if (r >= rows) break;
+          F2 x[P];
+          unpack_pairs<DT>(h[r][i], x);
+#pragma unroll
+          for (int q = 0; q < P; ++q)
+            x[q] = fma2((x[q] + f2(-mean[r])) * f2(rstd[r]), g[q], b[q]);
+          put_window<DT, false>(y + static_cast<int64_t>(r) * rr.classes * a.H, a.H, at * VE - off, x);
+        }
+      }
+    }
+    if (tid < 32 && more) rr.put_edges(st, j + S * rr.step, lane, ends);
+    if (G == 32) __syncwarp();
+    if (++st == S) st = 0, ++lap;
+  }
+  if (!ok && tid == 0) rr.drain(st, lap, j, S);
+}
+
+// Backward. A group reads the rows of a stage once (kHold: they stay packed in its registers) or
+// twice, and exchanges the sums of K tokens at once. Each thread keeps its columns' gradient sums in
+// registers over all its tokens: 16 columns at 512 threads an SM, which is what they and two held
+// rows leave room for. All waits are bounded, and a group leaves its loop together.
+template <int DT, int WT, int N, int K, bool kHold, bool kAligned>
+__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a, int G, int R,
+                                                            int S, int C) {
+  using E = Elem<DT>;
+  using W = Elem<WT>;
+  using raw = typename E::raw;
+  constexpr int VE = E::kVec, P = VE / 2;  // elements and pairs of a window
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kRingStages];
+  __shared__ float red[2][2 * K * 16];  // by turn: each warp's sums (joined_sums)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R * S; ++i) mbar_init(&full[i], 1);
+    fence_mbarrier_init();
+  }
+  RowRing<DT, 2, K, kAligned> rr;
+  rr.init(a.T, a.H, C, R, group, S, ring, full);
+  raw* const dx0 = static_cast<raw*>(a.dx) + static_cast<int64_t>(rr.cls) * a.H;
+  const int off = kAligned ? 0 : window_offset<DT>(dx0);
+  const int n = kAligned ? a.H / VE : window_count<DT>(off, a.H);
+  rr.array(0, a.x, a.x_stride, off);
+  rr.array(1, a.dy, a.dy_stride, off);
+  float* const gs = reinterpret_cast<float*>(ring + static_cast<size_t>(R * S) * rr.stage_bytes());
+  pdl_wait();
+  pdl_trigger();
+  stage_weights<VE, W>(gs, static_cast<const typename W::raw*>(a.gamma), 1.0f, a.H, off, n);
+  __syncthreads();
+  raw ends[K];
+  if (tid < 32)
+    for (int i = 0; i < S && rr.first + i * rr.step < rr.T; ++i) {
+      rr.copy(i, rr.first + i * rr.step, lane, ends);
+      rr.put_edges(i, rr.first + i * rr.step, lane, ends);
+    }
+  __syncthreads();
+
   const float fh = static_cast<float>(a.H);
   F2 dg[N][P], db[N][P];
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int q = 0; q < P; ++q) dg[i][q] = f2(0.0f), db[i][q] = f2(0.0f);
-  auto weights = [&](int at, F2 (&g)[P]) {
-#pragma unroll
-    for (int q = 0; q < VW; q += 4) {
-      const float4 v = reinterpret_cast<const float4*>(gs)[q / 4 * n + at];
-      g[q / 2] = f2(v.x, v.y);
-      g[q / 2 + 1] = f2(v.z, v.w);
-    }
-  };
-  auto pairs = [&](const uint4& w, F2 (&v)[P]) {
-    float f[VW];
-    E::unpack(w, f);
-#pragma unroll
-    for (int q = 0; q < P; ++q) v[q] = f2(f[2 * q], f[2 * q + 1]);
-  };
   float mean[K], rstd[K];
-  auto stats = [&](int64_t t) {
+  auto stats = [&](uint32_t j) {
 #pragma unroll
     for (int r = 0; r < K; ++r)
-      if (t + r < a.T) mean[r] = a.mean[t + r], rstd[r] = a.rstd[t + r];
+      if (j + r < rr.T) mean[r] = a.mean[rr.token(j + r)], rstd[r] = a.rstd[rr.token(j + r)];
   };
   const int nw = G >> 5, w0 = group * nw;
 #pragma unroll
   for (int r = 0; r < K; ++r) mean[r] = rstd[r] = 0.0f;
-  stats(t);
+  stats(rr.first);
   int st = 0, turn = 0;
   uint32_t lap = 0;
   bool ok = true;
-  for (; t < a.T; t += step, turn ^= 1) {
+  uint32_t j = rr.first;
+  for (; j < rr.T; j += rr.step, turn ^= 1) {
     F2 nm[K], fr[K];
     float rs[K];
 #pragma unroll
     for (int r = 0; r < K; ++r) nm[r] = f2(-mean[r]), fr[r] = f2(rstd[r]), rs[r] = rstd[r];
-    const int rows = t + K <= a.T ? K : static_cast<int>(a.T - t);
-    ok = mbar_wait(&mine[st], lap & 1, 130);
-    const uint4* const sx =
-        reinterpret_cast<const uint4*>(stages + static_cast<size_t>(st) * stage_bytes);
+    const int rows = rr.rows(j);
+    ok = mbar_wait(&rr.full[st], lap & 1, 130);
     uint4 hx[K][N], hd[K][N];
     if constexpr (kHold) {
 #pragma unroll
@@ -427,14 +763,14 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a,
         for (int i = 0; i < N; ++i) {
           const int at = i * G + tid;
           if (at < n && r < rows) {
-            hx[r][i] = sx[2 * r * n + at];
-            hd[r][i] = sx[(2 * r + 1) * n + at];
+            hx[r][i] = rr.window(st, r, 0, at, off);
+            hd[r][i] = rr.window(st, r, 1, at, off);
           } else {
             hx[r][i] = hd[r][i] = make_uint4(0, 0, 0, 0);
           }
         }
     }
-    stats(t + step);
+    stats(j + rr.step);
     F2 s1[K], s2[K];
 #pragma unroll
     for (int r = 0; r < K; ++r) s1[r] = s2[r] = f2(0.0f);
@@ -443,12 +779,12 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a,
       const int at = i * G + tid;
       if (at < n) {
         F2 g[P];
-        weights(at, g);
+        staged_weights<VE>(gs, n, at, g);
 #pragma unroll
         for (int r = 0; r < K; ++r) {
           F2 x[P], d[P];
-          pairs(kHold ? hx[r][i] : sx[2 * r * n + at], x);
-          pairs(kHold ? hd[r][i] : sx[(2 * r + 1) * n + at], d);
+          unpack_pairs<DT>(kHold ? hx[r][i] : rr.window(st, r, 0, at, off), x);
+          unpack_pairs<DT>(kHold ? hd[r][i] : rr.window(st, r, 1, at, off), d);
 #pragma unroll
           for (int q = 0; q < P; ++q) {  // a row that is not there has d_y = 0
             const F2 xh = (x[q] + nm[r]) * fr[r], v = d[q] * g[q];
@@ -478,12 +814,10 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a,
     }
     if (!ok) break;
     // Every thread has read this stage (kHold), or the one before for the last time.
-    if (kHold) {
-      if (tid == 0 && t + S * step < a.T) copy(st, t + S * step);
-    } else {
-      if (tid == 0 && lap + st > 0 && t + (S - 1) * step < a.T)
-        copy(st > 0 ? st - 1 : S - 1, t + (S - 1) * step);
-    }
+    const uint32_t next = j + (kHold ? S : S - 1) * rr.step;
+    const int free = kHold ? st : st > 0 ? st - 1 : S - 1;
+    const bool more = tid < 32 && next < rr.T && (kHold || lap + st > 0);
+    if (more) rr.copy(free, next, lane, ends);
     // d_x = r v - r c1 - (x - mean) r^2 c2
     F2 f1[K], fx[K];
 #pragma unroll
@@ -491,61 +825,69 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a,
       f1[r] = f2(-rs[r] * (sums[2 * r] / fh));
       fx[r] = f2(-rs[r] * rs[r] * (sums[2 * r + 1] / fh));
     }
-    raw* dx = static_cast<raw*>(a.dx) + t * a.H;
+    raw* const dx = dx0 + static_cast<int64_t>(j) * rr.classes * a.H;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int at = i * G + tid;
       if (at < n) {
         F2 g[P];
-        weights(at, g);
+        staged_weights<VE>(gs, n, at, g);
 #pragma unroll
         for (int r = 0; r < K; ++r) {
           if (r >= rows) break;
           F2 x[P], d[P];
-          pairs(kHold ? hx[r][i] : sx[2 * r * n + at], x);
-          pairs(kHold ? hd[r][i] : sx[(2 * r + 1) * n + at], d);
-          float o[VW];
+          unpack_pairs<DT>(kHold ? hx[r][i] : rr.window(st, r, 0, at, off), x);
+          unpack_pairs<DT>(kHold ? hd[r][i] : rr.window(st, r, 1, at, off), d);
 #pragma unroll
-          for (int q = 0; q < P; ++q) {
-            const float2 u = split(fma2(d[q] * g[q], fr[r], fma2(x[q] + nm[r], fx[r], f1[r])));
-            o[2 * q] = u.x, o[2 * q + 1] = u.y;
-          }
-          st_stream(dx + static_cast<int64_t>(r) * a.H + at * VW, E::pack(o));
+          for (int q = 0; q < P; ++q)
+            x[q] = fma2(d[q] * g[q], fr[r], fma2(x[q] + nm[r], fx[r], f1[r]));
+          put_window<DT, kAligned>(dx + static_cast<int64_t>(r) * rr.classes * a.H, a.H,
+                                   at * VE - off, x);
         }
       }
     }
+    if constexpr (!kAligned) {
+      if (more) rr.put_edges(free, next, lane, ends);
+      if (G == 32)
+        __syncwarp();
+      else if (!kHold && S == 2)  // the stage is the next one
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(G) : "memory");
+    }
     if (++st == S) st = 0, ++lap;
   }
-  if (!ok && tid == 0) {  // no copy into this CTA's shared memory may outlive it
-    const int ahead = kHold ? S : S - 1;  // stages with a copy from the current one on
-    for (int i = 0; i < S && t + i * step < a.T; ++i) {
-      if (i >= ahead && lap > 0) break;
-      mbar_wait(&mine[st], lap & 1, 131);
-      if (++st == S) st = 0, ++lap;
-    }
-  }
+  // Stages with a copy, from the current one on (the first pass of !kHold has them all).
+  if (!ok && tid == 0) rr.drain(st, lap, j, kHold || lap + st == 0 ? S : S - 1);
   if (!a.part) return;
   // The groups' sums, through the stages' memory (free: every group is done).
   __syncthreads();
-  float4* part = reinterpret_cast<float4*>(a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H);
-  float4* to = R > 1 ? reinterpret_cast<float4*>(ring) + static_cast<size_t>(group) * (a.H / 2)
-                     : part;
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
+  float* to = R > 1 ? reinterpret_cast<float*>(ring) + static_cast<size_t>(group) * (2 * a.H) : part;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int at = i * G + tid;
+    const int at = i * G + tid, e0 = at * VE - off;
     if (at < n) {
+      if (kAligned) {
 #pragma unroll
-      for (int q = 0; q < P; q += 2) {
-        const float2 lo = split(dg[i][q]), hi = split(dg[i][q + 1]);
-        to[at * (VW / 4) + q / 2] = make_float4(lo.x, lo.y, hi.x, hi.y);
-        const float2 lb = split(db[i][q]), hb = split(db[i][q + 1]);
-        to[a.H / 4 + at * (VW / 4) + q / 2] = make_float4(lb.x, lb.y, hb.x, hb.y);
+        for (int q = 0; q < P; q += 2) {
+          const float2 lo = split(dg[i][q]), hi = split(dg[i][q + 1]);
+          *reinterpret_cast<float4*>(to + e0 + 2 * q) = make_float4(lo.x, lo.y, hi.x, hi.y);
+          const float2 lb = split(db[i][q]), hb = split(db[i][q + 1]);
+          *reinterpret_cast<float4*>(to + a.H + e0 + 2 * q) = make_float4(lb.x, lb.y, hb.x, hb.y);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+          const float2 u = split(dg[i][q]), v = split(db[i][q]);
+          const int e = e0 + 2 * q;
+          if (e >= 0 && e < a.H) to[e] = u.x, to[a.H + e] = v.x;
+          if (e + 1 >= 0 && e + 1 < a.H) to[e + 1] = u.y, to[a.H + e + 1] = v.y;
+        }
       }
     }
   }
   if (R == 1) return;
   __syncthreads();
-  add_groups(reinterpret_cast<const float*>(ring), R, 2 * a.H, reinterpret_cast<float*>(part));
+  add_groups(reinterpret_cast<const float*>(ring), R, 2 * a.H, part);
 }
 
 // ------------------------------------------------------------------------------ any row
@@ -691,7 +1033,10 @@ __global__ void __launch_bounds__(kSumLanes* kSumRows) norm_bwd_sum_kernel(
 
 namespace {
 
-int norm_part_rows(int64_t T) { return static_cast<int>(T < kNormPartRows ? T : kNormPartRows); }
+// One per token at most, or (classes of tokens, RowRing) seven more.
+int norm_part_rows(int64_t T) {
+  return static_cast<int>(T + 7 < kNormPartRows ? T + 7 : kNormPartRows);
+}
 
 unsigned row_grid(int64_t T) {
   const int64_t cap = static_cast<int64_t>(device_sm_count()) * 64;
@@ -742,25 +1087,72 @@ cudaError_t norm_forward_rows(const NormArgs& a, cudaStream_t s, bool* done) {
   return cudaSuccess;
 }
 
-template <int DT, int WT>
-int norm_forward(const NormArgs& a, cudaStream_t s) {
-  constexpr int VE = Elem<DT>::kVec;
-  bool done = false;
-  cudaError_t e;
-  if (vector_rows(VE, a.H, {a.x_stride}, {a.x, a.y, a.gamma, a.beta}))
-    e = norm_forward_rows<DT, WT, VE>(a, s, &done);
-  else
-    e = norm_forward_rows<DT, WT, 1>(a, s, &done);
-  if (!done)
-    e = launch_pdl(norm_loop_kernel<DT, WT>, dim3(row_grid(a.T)), dim3(kNormThreads), 0, s, a);
-  note_launches(1);
-  return e == cudaSuccess ? 0 : MHC_ERR_CUDA;
-}
-
 // CTAs of a backward kernel: one an SM (a device-independent bound keeps the workspace the same).
 unsigned norm_bwd_grid(int64_t most) {
   const int64_t sms = device_sm_count() < kNormPartRows ? device_sm_count() : kNormPartRows;
   return static_cast<unsigned>(most < sms ? most : sms);
+}
+
+// How a staged kernel of A arrays is launched: windows per thread and tokens per stage are its
+// template's.
+struct RingPlan {
+  int G, R, S, C;
+  unsigned grid;
+  size_t smem;
+  bool ok;
+};
+template <int VE>
+RingPlan ring_plan(int64_t T, int64_t H, int A, int per, int K, int weights, bool aligned,
+                   bool sums) {
+  RingPlan p{};
+  const int n = static_cast<int>(aligned ? H / VE : (H + 2 * VE - 2) / VE);
+  p.G = round32((n + per - 1) / per);
+  if (p.G > 512 || H < 2 * VE) return p;
+  p.R = p.G == 32 ? 16 : 512 / p.G < 15 ? 512 / p.G : 15;
+  p.C = aligned ? 1 : VE;
+  const size_t stage = static_cast<size_t>(A) * K * (aligned ? n : n + 2) * 16;
+  const size_t w = static_cast<size_t>(weights) * n * VE * 4;
+  const size_t limit = 224 * 1024;
+  if (w >= limit) return p;
+  const size_t fit = (limit - w) / (stage * p.R);
+  p.S = static_cast<int>(fit < kRingStages / 16 ? fit : kRingStages / 16);
+  if (p.S < 2) return p;
+  p.smem = p.R * p.S * stage + w;
+  // the groups' sums may overwrite the stages and the weights behind them
+  const size_t sum = sums && p.R > 1 ? static_cast<size_t>(p.R) * 2 * H * 4 : 0;
+  if (p.smem < sum) p.smem = sum;
+  const int64_t batches = (T + static_cast<int64_t>(p.C) * K - 1) / (static_cast<int64_t>(p.C) * K);
+  const int64_t most = norm_bwd_grid(kNormPartRows) / p.C;
+  p.grid = static_cast<unsigned>((batches < most ? batches : most) * p.C);
+  p.ok = p.grid > 0;
+  return p;
+}
+
+template <int DT, int WT>
+cudaError_t norm_forward_ring(const NormArgs& a, cudaStream_t s, bool* done) {
+  constexpr int VE = Elem<DT>::kVec, N = 16 / VE;
+  const bool wide = (a.H + 2 * VE - 2) / VE > 512 * N;
+  const RingPlan p = ring_plan<VE>(a.T, a.H, 1, wide ? 2 * N : N, 2, 2, false, false);
+  auto k = wide ? norm_ring_kernel<DT, WT, 2 * N, 2> : norm_ring_kernel<DT, WT, N, 2>;
+  *done = p.ok && ensure_smem_limit(reinterpret_cast<const void*>(k), static_cast<int>(p.smem));
+  if (!*done) return cudaSuccess;
+  return launch_pdl(k, dim3(p.grid), dim3(p.G * p.R), p.smem, s, a, p.G, p.R, p.S, p.C);
+}
+
+template <int DT, int WT>
+int norm_forward(const NormArgs& a, cudaStream_t s) {
+  constexpr int VE = Elem<DT>::kVec;
+  bool done = false;
+  cudaError_t e = cudaSuccess;
+  if (vector_rows(VE, a.H, {a.x_stride}, {a.x, a.y, a.gamma, a.beta}))
+    e = norm_forward_rows<DT, WT, VE>(a, s, &done);
+  else if (a.T >= 2 * device_sm_count())
+    e = norm_forward_ring<DT, WT>(a, s, &done);
+  if (!done) e = norm_forward_rows<DT, WT, 1>(a, s, &done);
+  if (!done)
+    e = launch_pdl(norm_loop_kernel<DT, WT>, dim3(row_grid(a.T)), dim3(kNormThreads), 0, s, a);
+  note_launches(1);
+  return e == cudaSuccess ? 0 : MHC_ERR_CUDA;
 }
 
 // Launches the element-wise form and returns its number of partial rows, or 0 (nothing launched)
@@ -780,33 +1172,23 @@ int norm_backward_rows(const NormBwdArgs& a, cudaStream_t s, cudaError_t* e) {
   return static_cast<int>(grid);
 }
 
-// The staged form, likewise: rows of 16-byte accesses that fit twice beside gamma.
-template <int DT, int WT>
+// The staged form, likewise: rows that fit twice beside gamma.
+template <int DT, int WT, bool kAligned>
 int norm_backward_ring(const NormBwdArgs& a, cudaStream_t s, cudaError_t* e) {
-  constexpr int VW = Elem<DT>::kVec, N = 16 / VW;  // accesses of a thread that holds 16 columns
-  constexpr int K = VW == 8 ? 2 : 1;
-  const int64_t n = a.H / VW;
+  constexpr int VE = Elem<DT>::kVec, N = 16 / VE;  // windows of a thread that holds 16 columns
+  constexpr int K = VE == 8 ? 2 : 1;
+  const int n = static_cast<int>(kAligned ? a.H / VE : (static_cast<int64_t>(a.H) + 2 * VE - 2) / VE);
   const bool hold = n <= 512 * N;
-  const int per = hold ? (n <= 32 ? 1 : N) : 2 * N;
-  const int G = round32((n + per - 1) / per);
-  if (G > 512) return 0;
-  const int R = G == 32 ? 16 : 512 / G < 15 ? 512 / G : 15;
-  const size_t stage = 2 * static_cast<size_t>(a.H) * sizeof(typename Elem<DT>::raw) * (hold ? K : 1);
-  const size_t weights = static_cast<size_t>(a.H) * 4, sums = R > 1 ? 2 * weights * R : 0;
-  const size_t fit = (224 * 1024 - weights) / (stage * R);
-  const int S = static_cast<int>(fit < kRingStages / 16 ? fit : kRingStages / 16);
-  if (S < 2) return 0;
-  // gamma lies behind the stages; the groups' sums may overwrite it
-  const size_t used = R * S * stage + weights, smem = used > sums ? used : sums;
-  auto k = !hold      ? norm_bwd_ring_kernel<DT, WT, 2 * N, 1, false>
-           : per == 1 ? norm_bwd_ring_kernel<DT, WT, 1, K, true>
-                      : norm_bwd_ring_kernel<DT, WT, N, K, true>;
-  if (!ensure_smem_limit(reinterpret_cast<const void*>(k), static_cast<int>(smem))) return 0;
-  const int rows = hold ? K : 1;
-  const unsigned grid = norm_bwd_grid((a.T + rows - 1) / rows);
-  *e = launch_pdl(k, dim3(grid), dim3(G * R), smem, s, a, G, R, S);
+  const int per = !hold ? 2 * N : n <= 32 ? 1 : N;
+  const RingPlan p = ring_plan<VE>(a.T, a.H, 2, per, hold ? K : 1, 1, kAligned, true);
+  if (!p.ok) return 0;
+  auto k = !hold      ? norm_bwd_ring_kernel<DT, WT, 2 * N, 1, false, kAligned>
+           : per == 1 ? norm_bwd_ring_kernel<DT, WT, 1, K, true, kAligned>
+                      : norm_bwd_ring_kernel<DT, WT, N, K, true, kAligned>;
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(k), static_cast<int>(p.smem))) return 0;
+  *e = launch_pdl(k, dim3(p.grid), dim3(p.G * p.R), p.smem, s, a, p.G, p.R, p.S, p.C);
   note_launches(1);
-  return static_cast<int>(grid);
+  return static_cast<int>(p.grid);
 }
 
 template <int DT, int WT>
@@ -816,8 +1198,10 @@ int norm_backward(NormBwdArgs a, float* dgamma, float* dbeta, cudaStream_t s) {
   if (!params) a.part = nullptr;
   cudaError_t e = cudaSuccess;
   int rows = 0;
-  if (vector_rows(VE, a.H, {a.x_stride, a.dy_stride}, {a.x, a.dy, a.dx, a.gamma}))
-    rows = norm_backward_ring<DT, WT>(a, s, &e);
+  if (vector_rows(VE, a.H, {a.x_stride, a.dy_stride}, {a.x, a.dy, a.dx}))
+    rows = norm_backward_ring<DT, WT, true>(a, s, &e);
+  else
+    rows = norm_backward_ring<DT, WT, false>(a, s, &e);
   if (rows == 0) rows = norm_backward_rows<DT, WT>(a, s, &e);
   if (rows == 0) {
     e = launch_pdl(norm_bwd_dx_loop_kernel<DT, WT>, dim3(row_grid(a.T)), dim3(kNormThreads), 0, s,
