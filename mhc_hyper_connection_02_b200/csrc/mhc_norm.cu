@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(512) norm_bwd_row_kernel(const NormBwdArgs a, 
   using E = Elem<DT>;
   using raw = typename E::raw;
   extern __shared__ float group_sums[];  // [R][2][H] (R > 1)
-  __shared__ float red[2][2 * 16];       // by turn: each warp's sums (joined_sums)
+  __shared__ float red[2][2 * 32];       // by turn: each warp's sums (joined_sums)
   pdl_wait();
   pdl_trigger();
   const int R = blockDim.x / G;
@@ -333,8 +333,11 @@ __global__ void __launch_bounds__(512) norm_bwd_row_kernel(const NormBwdArgs a, 
 // its first window (its phase) repeats every kVec tokens, so a CTA takes tokens of one class t mod
 // kVec only. Then every row of an array has the same phase there, columns stay with their threads,
 // and all accesses are whole windows. The output's phase sets the windows; an input of another phase
-// (a gap between its rows) is read as two windows and shifted. Bulk copies take the windows that the
-// row fills, single loads the up to kVec - 1 elements at either end.
+// (a gap between its rows) is read as two windows and shifted. The copies take whole windows too:
+// what they read beside a row belongs to the rows before and after it (or the gap between) and is
+// not used; only before the first token's row and behind the last one's, where the array ends, the
+// row's own elements are read one by one.
+constexpr int kStagesEach = 4;  // of a group, at most
 template <int DT, int A, int K, bool kAligned>
 struct RowRing {
   using E = Elem<DT>;
@@ -346,22 +349,29 @@ struct RowRing {
   int shift[A];       // against the output's phase
   // Tokens are below 2^31; a few stages beyond the last still fit 32 bits.
   uint32_t T;            // tokens of the class
+  int64_t tokens;        // of all
   uint32_t first, step;  // in the class: the group's first, and from one stage to its next
   int H, classes, cls;
   int slot;           // windows of a row in a stage
   uint8_t* stages;
   uint64_t* full;
+  float* stats;       // per stage: K pairs of mean and rstd (A = 2)
+  const float* mean;  // of the class's tokens
+  const float* rstd;
   int S;
 
   // Windows of a slot: those a row of n elements touches and, unaligned, one before and one after.
   static __host__ __device__ __forceinline__ int slot_windows(int n) {
     return kAligned ? n / VE : (n + 2 * VE - 2) / VE + 2;
   }
-  __device__ __forceinline__ void init(int64_t tokens, int h, int C, int groups, int group,
-                                       int stages_each, uint8_t* memory, uint64_t* bars) {
+  __device__ __forceinline__ void init(int64_t all, int h, int C, int groups, int group,
+                                       int stages_each, uint8_t* memory, uint64_t* bars,
+                                       float* pairs = nullptr, const float* means = nullptr,
+                                       const float* rstds = nullptr) {
     classes = kAligned ? 1 : C;
     cls = blockIdx.x % classes;
     const int rank = blockIdx.x / classes, ranks = gridDim.x / classes;
+    tokens = all;
     T = static_cast<uint32_t>((tokens - cls + classes - 1) / classes);
     first = (group * ranks + rank) * K;
     step = ranks * K * groups;
@@ -369,6 +379,15 @@ struct RowRing {
     slot = slot_windows(h);
     stages = memory + static_cast<size_t>(group * S) * stage_bytes();
     full = bars + group * S;
+    if constexpr (A == 2) {
+      stats = pairs + group * S * 2 * K;
+      mean = means + cls, rstd = rstds + cls;
+    }
+  }
+  // By one thread, before anything is copied.
+  static __device__ __forceinline__ void init_barriers(uint64_t* bars, int n) {
+    for (int i = 0; i < n; ++i) mbar_init(&bars[i], A);  // bulk copies; A = 2: and the statistics
+    fence_mbarrier_init();
   }
   __device__ __forceinline__ void array(int i, const void* p, int64_t st, int out_off) {
     base[i] = static_cast<const raw*>(p) + cls * st;
@@ -388,54 +407,58 @@ struct RowRing {
            (r * A + i) * slot;
   }
 
-  // The ends of a row: lane e of array i = lane / 16 takes one element, or none (-1).
-  __device__ __forceinline__ int edge(int lane) const {
-    const int o = A == 2 && lane >= 16 ? off[A - 1] : off[0], e = lane & 15;
-    if (A == 1 && lane >= 16) return -1;
-    if (e < 8) return o > 0 && e < VE - o ? e : -1;
-    const int at = (o + H) / VE * VE - o + e - 8;
-    return e - 8 < VE && at < H ? at : -1;
+  // Windows [from, to) of token t's row that are copied, and (unaligned) the elements that are not.
+  __device__ __forceinline__ int2 copied(int i, int64_t t) const {
+    const int end = off[i] + H;
+    return make_int2(t == 0 && off[i] > 0 ? 1 : 0,
+                     t == tokens - 1 ? end / VE : (end + VE - 1) / VE);
   }
-  // Starts the copy of the tokens j .. into a stage (the group's first warp) and reads the ends of
-  // their rows, which put_edges writes there.
-  __device__ __forceinline__ void copy(int st, uint32_t j, int lane, raw (&ends)[K]) const {
-    const int n = rows(j);
-    if (lane == 0) {
-      uint32_t bytes = 0;
-#pragma unroll
-      for (int i = 0; i < A; ++i)
-        bytes += kAligned ? H / VE : (off[i] + H) / VE - (off[i] > 0 ? 1 : 0);
-      mbar_arrive_expect_tx(&full[st], bytes * n * 16);
-      for (int r = 0; r < n; ++r)
+  // Starts the copy of the tokens j .. into a stage (one thread). A stage that the class's last
+  // token does not fill gets that token again.
+  __device__ __forceinline__ void copy(int st, uint32_t j) const {
+    uint32_t bytes = A * K * (H / VE) * 16;
+    if constexpr (!kAligned) {
+      bytes = 0;
+      for (int r = 0; r < K; ++r)
 #pragma unroll
         for (int i = 0; i < A; ++i) {
-          const int from = off[i] > 0 ? 1 : 0;  // the first window that the row fills
-          const raw* row = base[i] + static_cast<int64_t>(j + r) * stride[i];
-          bulk_g2s(slot_at(st, r, i) + (kAligned ? 0 : 1 + from),
-                   row + (from ? VE - off[i] : 0),
-                   ((kAligned ? 0 : off[i]) + H) / VE * 16 - from * 16, &full[st]);
+          const int2 w = copied(i, token(min(j + r, T - 1)));
+          bytes += (w.y - w.x) * 16;
         }
     }
-    if constexpr (!kAligned) {
-      const int at = edge(lane);
-      const bool second = A == 2 && lane >= 16;
-      const raw* from = second ? base[A - 1] : base[0];
-      const int64_t st_r = second ? stride[A - 1] : stride[0];
+    mbar_arrive_expect_tx(&full[st], bytes);
 #pragma unroll
-      for (int r = 0; r < K; ++r)
-        if (at >= 0 && r < n) ends[r] = from[static_cast<int64_t>(j + r) * st_r + at];
+    for (int r = 0; r < K; ++r)
+#pragma unroll
+      for (int i = 0; i < A; ++i) {
+        const uint32_t at = min(j + r, T - 1);
+        const raw* row = base[i] + static_cast<int64_t>(at) * stride[i];
+        uint4* to = slot_at(st, r, i);
+        if constexpr (kAligned) {
+          bulk_g2s(to, row, H / VE * 16, &full[st]);
+        } else {
+          const int2 w = copied(i, token(at));
+          ++to;
+          raw* elements = reinterpret_cast<raw*>(to) + off[i];
+          if (w.x > 0)
+            for (int e = 0; e < VE - off[i]; ++e) elements[e] = row[e];
+          for (int e = w.y * VE - off[i]; e < H; ++e) elements[e] = row[e];
+          bulk_g2s(to + w.x, row - off[i] + w.x * VE, (w.y - w.x) * 16, &full[st]);
+        }
+      }
+    if constexpr (A == 2) {
+#pragma unroll
+      for (int r = 0; r < K; ++r) {
+        const int64_t t = static_cast<int64_t>(min(j + r, T - 1)) * classes;
+        async_copy4(&stats[(st * K + r) * 2], mean + t);
+        async_copy4(&stats[(st * K + r) * 2 + 1], rstd + t);
+      }
+      async_copies_arrive(&full[st]);
     }
   }
-  __device__ __forceinline__ void put_edges(int st, uint32_t j, int lane, const raw (&ends)[K]) const {
-    if constexpr (!kAligned) {
-      const int n = rows(j), at = edge(lane);
-      const bool second = A == 2 && lane >= 16;
-      const int o = second ? off[A - 1] : off[0];
-#pragma unroll
-      for (int r = 0; r < K; ++r)
-        if (at >= 0 && r < n)
-          reinterpret_cast<raw*>(slot_at(st, r, second ? 1 : 0) + 1)[o + at] = ends[r];
-    }
+  // The first S stages.
+  __device__ __forceinline__ void start() const {
+    for (int i = 0; i < S && first + i * step < T; ++i) copy(i, first + i * step);
   }
 
   // Output window s of row r of array i; what lies outside the row comes back as zero.
@@ -492,10 +515,19 @@ struct RowRing {
 template <int VE, typename W>
 __device__ __forceinline__ void stage_weights(float* to, const typename W::raw* w, float otherwise,
                                               int H, int off, int n) {
-  for (int i = threadIdx.x; i < n * VE; i += blockDim.x) {
-    const int h = i - off;
-    to[((i % VE) / 4 * n + i / VE) * 4 + i % 4] =
-        h < 0 || h >= H ? 0.0f : w ? W::to_f32(w[h]) : otherwise;
+  constexpr int U = 8;  // loads in flight
+  for (int i0 = threadIdx.x; i0 < n * VE; i0 += U * blockDim.x) {
+    float v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = i0 + u * blockDim.x - off;
+      v[u] = h < 0 || h >= H ? 0.0f : w ? W::to_f32(__ldg(w + h)) : otherwise;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * blockDim.x;
+      if (i < n * VE) to[((i % VE) / 4 * n + i / VE) * 4 + i % 4] = v[u];
+    }
   }
 }
 template <int VE>
@@ -534,11 +566,12 @@ __device__ __forceinline__ void put_window(typename Elem<DT>::raw* row, int H, i
   }
 }
 
-constexpr int kRingStages = 64;  // of all groups, at most
+constexpr int kRingStages = 64;    // of all groups, at most
+constexpr int kRingThreads = 512;  // of all groups, at most
 
 // Forward of rows that are not whole windows. x is read once and stays packed in registers.
 template <int DT, int WT, int N, int K>
-__global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a, int G, int R, int S,
+__global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs a, int G, int R, int S,
                                                         int C) {
   using E = Elem<DT>;
   using W = Elem<WT>;
@@ -546,14 +579,12 @@ __global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a, int G,
   constexpr int VE = E::kVec, P = VE / 2;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kRingStages];
-  __shared__ float red[2][2 * 16];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float red[2][2 * 32];
+  const int warp = threadIdx.x >> 5;
   const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < R * S; ++i) mbar_init(&full[i], 1);
-    fence_mbarrier_init();
-  }
-  RowRing<DT, 1, K, false> rr;
+  using Ring = RowRing<DT, 1, K, false>;
+  if (threadIdx.x == 0) Ring::init_barriers(full, R * S);
+  Ring rr;
   rr.init(a.T, a.H, C, R, group, S, ring, full);
   raw* const y0 = static_cast<raw*>(a.y) + static_cast<int64_t>(rr.cls) * a.H;
   const int off = window_offset<DT>(y0), n = window_count<DT>(off, a.H);
@@ -562,19 +593,14 @@ __global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a, int G,
   float* const bs = gs + n * VE;
   pdl_wait();
   pdl_trigger();
+  __syncthreads();
+  const int nw = G >> 5, w0 = group * nw;
+  if (tid == 0) rr.start();
   stage_weights<VE, W>(gs, static_cast<const typename W::raw*>(a.gamma), 1.0f, a.H, off, n);
   stage_weights<VE, W>(bs, static_cast<const typename W::raw*>(a.beta), 0.0f, a.H, off, n);
   __syncthreads();
-  raw ends[K];
-  if (tid < 32)
-    for (int i = 0; i < S && rr.first + i * rr.step < rr.T; ++i) {
-      rr.copy(i, rr.first + i * rr.step, lane, ends);
-      rr.put_edges(i, rr.first + i * rr.step, lane, ends);
-    }
-  __syncthreads();
 
   const float fh = static_cast<float>(a.H);
-  const int nw = G >> 5, w0 = group * nw;
   int turn = 0;
   bool ok = true;
   auto total = [&](const float (&v)[K], float (&out)[K]) {  // over the group, which agrees on ok
@@ -606,7 +632,7 @@ __global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a, int G,
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int at = i * G + tid;
-        h[r][i] = at < n && r < rows ? rr.window(st, r, 0, at, off) : make_uint4(0, 0, 0, 0);
+        h[r][i] = at < n ? rr.window(st, r, 0, at, off) : make_uint4(0, 0, 0, 0);
         F2 x[P];
         unpack_pairs<DT>(h[r][i], x);
 #pragma unroll
@@ -617,9 +643,8 @@ __global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a, int G,
     }
     total(s, mean);
     if (!ok) break;
-    const bool more = j + S * rr.step < rr.T;
     if (G == 32) __syncwarp();
-    if (tid < 32 && more) rr.copy(st, j + S * rr.step, lane, ends);
+    if (tid == 0 && j + S * rr.step < rr.T) rr.copy(st, j + S * rr.step);
 #pragma unroll
     for (int r = 0; r < K; ++r) {
       mean[r] /= fh;
@@ -681,8 +706,6 @@ __global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a, int G,
         }
       }
     }
-    if (tid < 32 && more) rr.put_edges(st, j + S * rr.step, lane, ends);
-    if (G == 32) __syncwarp();
     if (++st == S) st = 0, ++lap;
   }
   if (!ok && tid == 0) rr.drain(st, lap, j, S);
@@ -693,7 +716,7 @@ __global__ void __launch_bounds__(512) norm_ring_kernel(const NormArgs a, int G,
 // registers over all its tokens: 16 columns at 512 threads an SM, which is what they and two held
 // rows leave room for. All waits are bounded, and a group leaves its loop together.
 template <int DT, int WT, int N, int K, bool kHold, bool kAligned>
-__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a, int G, int R,
+__global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormBwdArgs a, int G, int R,
                                                             int S, int C) {
   using E = Elem<DT>;
   using W = Elem<WT>;
@@ -701,60 +724,79 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a,
   constexpr int VE = E::kVec, P = VE / 2;  // elements and pairs of a window
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kRingStages];
-  __shared__ float red[2][2 * K * 16];  // by turn: each warp's sums (joined_sums)
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float red[2][2 * K * 32];  // by turn: each warp's sums (joined_sums)
+  const int warp = threadIdx.x >> 5;
   const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < R * S; ++i) mbar_init(&full[i], 1);
-    fence_mbarrier_init();
-  }
-  RowRing<DT, 2, K, kAligned> rr;
-  rr.init(a.T, a.H, C, R, group, S, ring, full);
+  __shared__ __align__(8) float stats[kRingStages * 2 * K];
+  using Ring = RowRing<DT, 2, K, kAligned>;
+  if (threadIdx.x == 0) Ring::init_barriers(full, R * S);
+  Ring rr;
+  rr.init(a.T, a.H, C, R, group, S, ring, full, stats, a.mean, a.rstd);
   raw* const dx0 = static_cast<raw*>(a.dx) + static_cast<int64_t>(rr.cls) * a.H;
   const int off = kAligned ? 0 : window_offset<DT>(dx0);
   const int n = kAligned ? a.H / VE : window_count<DT>(off, a.H);
   rr.array(0, a.x, a.x_stride, off);
   rr.array(1, a.dy, a.dy_stride, off);
-  float* const gs = reinterpret_cast<float*>(ring + static_cast<size_t>(R * S) * rr.stage_bytes());
   pdl_wait();
   pdl_trigger();
-  stage_weights<VE, W>(gs, static_cast<const typename W::raw*>(a.gamma), 1.0f, a.H, off, n);
   __syncthreads();
-  raw ends[K];
-  if (tid < 32)
-    for (int i = 0; i < S && rr.first + i * rr.step < rr.T; ++i) {
-      rr.copy(i, rr.first + i * rr.step, lane, ends);
-      rr.put_edges(i, rr.first + i * rr.step, lane, ends);
+  const int nw = G >> 5, w0 = group * nw;
+  if (tid == 0) rr.start();
+  // gamma: in registers (kHold), or behind the stages.
+  const auto* const gamma = static_cast<const typename W::raw*>(a.gamma);
+  float* const gs = reinterpret_cast<float*>(ring + static_cast<size_t>(R * S) * rr.stage_bytes());
+  [[maybe_unused]] F2 own[kHold ? N : 1][P];
+  if constexpr (kHold) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float v[VE];
+#pragma unroll
+      for (int q = 0; q < VE; ++q) {
+        const int h = (i * G + tid) * VE - off + q;
+        v[q] = h < 0 || h >= a.H ? 0.0f : gamma ? W::to_f32(__ldg(gamma + h)) : 1.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < P; ++q) own[i][q] = f2(v[2 * q], v[2 * q + 1]);
     }
+  } else {
+    stage_weights<VE, W>(gs, gamma, 1.0f, a.H, off, n);
+  }
+  auto weights = [&](int i, int at, F2 (&g)[P]) {
+    if constexpr (kHold) {
+#pragma unroll
+      for (int q = 0; q < P; ++q) g[q] = own[i][q];
+    } else {
+      staged_weights<VE>(gs, n, at, g);
+    }
+  };
   __syncthreads();
+  constexpr int lag = kHold ? 0 : 1;  // the stage to copy into was read that many iterations ago
 
-  const float fh = static_cast<float>(a.H);
+  const float per_h = 1.0f / static_cast<float>(a.H);
   F2 dg[N][P], db[N][P];
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int q = 0; q < P; ++q) dg[i][q] = f2(0.0f), db[i][q] = f2(0.0f);
-  float mean[K], rstd[K];
-  auto stats = [&](uint32_t j) {
-#pragma unroll
-    for (int r = 0; r < K; ++r)
-      if (j + r < rr.T) mean[r] = a.mean[rr.token(j + r)], rstd[r] = a.rstd[rr.token(j + r)];
-  };
-  const int nw = G >> 5, w0 = group * nw;
-#pragma unroll
-  for (int r = 0; r < K; ++r) mean[r] = rstd[r] = 0.0f;
-  stats(rr.first);
+  raw* dx = dx0 + static_cast<int64_t>(rr.first) * rr.classes * a.H;
+  const int64_t dx_step = static_cast<int64_t>(rr.step) * rr.classes * a.H;
   int st = 0, turn = 0;
   uint32_t lap = 0;
   bool ok = true;
   uint32_t j = rr.first;
   for (; j < rr.T; j += rr.step, turn ^= 1) {
+    const int rows = rr.rows(j);
+    ok = mbar_wait(&rr.full[st], lap & 1, 130);
     F2 nm[K], fr[K];
     float rs[K];
 #pragma unroll
-    for (int r = 0; r < K; ++r) nm[r] = f2(-mean[r]), fr[r] = f2(rstd[r]), rs[r] = rstd[r];
-    const int rows = rr.rows(j);
-    ok = mbar_wait(&rr.full[st], lap & 1, 130);
+    for (int r = 0; r < K; ++r) {
+      const float2 v = reinterpret_cast<const float2*>(rr.stats)[st * K + r];
+      nm[r] = f2(-v.x);
+      rs[r] = v.y;
+      fr[r] = f2(rs[r]);
+    }
+    const bool whole = K == 1 || rows == K;  // else the last row is there twice
     uint4 hx[K][N], hd[K][N];
     if constexpr (kHold) {
 #pragma unroll
@@ -762,15 +804,13 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a,
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int at = i * G + tid;
-          if (at < n && r < rows) {
+          if (at < n) {
             hx[r][i] = rr.window(st, r, 0, at, off);
             hd[r][i] = rr.window(st, r, 1, at, off);
-          } else {
-            hx[r][i] = hd[r][i] = make_uint4(0, 0, 0, 0);
+            if (r > 0 && !whole) hx[r][i] = hd[r][i] = make_uint4(0, 0, 0, 0);
           }
         }
     }
-    stats(j + rr.step);
     F2 s1[K], s2[K];
 #pragma unroll
     for (int r = 0; r < K; ++r) s1[r] = s2[r] = f2(0.0f);
@@ -779,19 +819,19 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a,
       const int at = i * G + tid;
       if (at < n) {
         F2 g[P];
-        staged_weights<VE>(gs, n, at, g);
+        weights(i, at, g);
 #pragma unroll
         for (int r = 0; r < K; ++r) {
           F2 x[P], d[P];
           unpack_pairs<DT>(kHold ? hx[r][i] : rr.window(st, r, 0, at, off), x);
           unpack_pairs<DT>(kHold ? hd[r][i] : rr.window(st, r, 1, at, off), d);
 #pragma unroll
-          for (int q = 0; q < P; ++q) {  // a row that is not there has d_y = 0
-            const F2 xh = (x[q] + nm[r]) * fr[r], v = d[q] * g[q];
-            dg[i][q] = fma2(d[q], xh, dg[i][q]);
+          for (int q = 0; q < P; ++q) {
+            const F2 u = d[q] * (x[q] + nm[r]);
+            dg[i][q] = fma2(u, fr[r], dg[i][q]);
             db[i][q] = db[i][q] + d[q];
-            s1[r] = s1[r] + v;
-            s2[r] = fma2(v, xh, s2[r]);
+            s1[r] = fma2(d[q], g[q], s1[r]);
+            s2[r] = fma2(u, g[q], s2[r]);  // sum(q (x - mean))
           }
         }
       }
@@ -814,45 +854,40 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a,
     }
     if (!ok) break;
     // Every thread has read this stage (kHold), or the one before for the last time.
-    const uint32_t next = j + (kHold ? S : S - 1) * rr.step;
-    const int free = kHold ? st : st > 0 ? st - 1 : S - 1;
-    const bool more = tid < 32 && next < rr.T && (kHold || lap + st > 0);
-    if (more) rr.copy(free, next, lane, ends);
-    // d_x = r v - r c1 - (x - mean) r^2 c2
-    F2 f1[K], fx[K];
+    const uint32_t next = j + (S - lag) * rr.step;
+    if (G == 32) __syncwarp();
+    if (tid == 0 && (kHold || lap + st > 0) && next < rr.T)
+      rr.copy(kHold ? st : st > 0 ? st - 1 : S - 1, next);
+    // d_x = r d_y gamma - r c1 - (x - mean) r^2 c2 = r (d_y gamma) + (x f + f0). The mean's part of
+    // f0 is rounded against a product with c2, which is small where many columns make |mean| r large.
+    F2 f0[K], fx[K];
 #pragma unroll
     for (int r = 0; r < K; ++r) {
-      f1[r] = f2(-rs[r] * (sums[2 * r] / fh));
-      fx[r] = f2(-rs[r] * rs[r] * (sums[2 * r + 1] / fh));
+      const float f = -rs[r] * rs[r] * (rs[r] * sums[2 * r + 1] * per_h);
+      fx[r] = f2(f);
+      f0[r] = f2(fmaf(split(nm[r]).x, f, -rs[r] * (sums[2 * r] * per_h)));
     }
-    raw* const dx = dx0 + static_cast<int64_t>(j) * rr.classes * a.H;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int at = i * G + tid;
       if (at < n) {
         F2 g[P];
-        staged_weights<VE>(gs, n, at, g);
+        weights(i, at, g);
 #pragma unroll
         for (int r = 0; r < K; ++r) {
-          if (r >= rows) break;
+          if (r > 0 && !whole) break;
           F2 x[P], d[P];
           unpack_pairs<DT>(kHold ? hx[r][i] : rr.window(st, r, 0, at, off), x);
           unpack_pairs<DT>(kHold ? hd[r][i] : rr.window(st, r, 1, at, off), d);
 #pragma unroll
           for (int q = 0; q < P; ++q)
-            x[q] = fma2(d[q] * g[q], fr[r], fma2(x[q] + nm[r], fx[r], f1[r]));
+            x[q] = fma2(d[q] * g[q], fr[r], fma2(x[q], fx[r], f0[r]));
           put_window<DT, kAligned>(dx + static_cast<int64_t>(r) * rr.classes * a.H, a.H,
                                    at * VE - off, x);
         }
       }
     }
-    if constexpr (!kAligned) {
-      if (more) rr.put_edges(free, next, lane, ends);
-      if (G == 32)
-        __syncwarp();
-      else if (!kHold && S == 2)  // the stage is the next one
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(G) : "memory");
-    }
+    dx += dx_step;
     if (++st == S) st = 0, ++lap;
   }
   // Stages with a copy, from the current one on (the first pass of !kHold has them all).
@@ -1103,20 +1138,21 @@ struct RingPlan {
 };
 template <int VE>
 RingPlan ring_plan(int64_t T, int64_t H, int A, int per, int K, int weights, bool aligned,
-                   bool sums) {
+                   bool sums, int least) {
   RingPlan p{};
   const int n = static_cast<int>(aligned ? H / VE : (H + 2 * VE - 2) / VE);
   p.G = round32((n + per - 1) / per);
-  if (p.G > 512 || H < 2 * VE) return p;
-  p.R = p.G == 32 ? 16 : 512 / p.G < 15 ? 512 / p.G : 15;
+  if (p.G > kRingThreads || H < 2 * VE) return p;
+  p.R = kRingThreads / p.G < 15 ? kRingThreads / p.G : p.G == 32 ? kRingThreads / p.G : 15;
   p.C = aligned ? 1 : VE;
   const size_t stage = static_cast<size_t>(A) * K * (aligned ? n : n + 2) * 16;
-  const size_t w = static_cast<size_t>(weights) * n * VE * 4;
+  const size_t w = static_cast<size_t>(weights) * n * VE * 4;  // staged weights
   const size_t limit = 224 * 1024;
   if (w >= limit) return p;
   const size_t fit = (limit - w) / (stage * p.R);
-  p.S = static_cast<int>(fit < kRingStages / 16 ? fit : kRingStages / 16);
-  if (p.S < 2) return p;
+  const size_t most_stages = kRingStages / p.R < kStagesEach ? kRingStages / p.R : kStagesEach;
+  p.S = static_cast<int>(fit < most_stages ? fit : most_stages);
+  if (p.S < least) return p;
   p.smem = p.R * p.S * stage + w;
   // the groups' sums may overwrite the stages and the weights behind them
   const size_t sum = sums && p.R > 1 ? static_cast<size_t>(p.R) * 2 * H * 4 : 0;
@@ -1131,8 +1167,8 @@ RingPlan ring_plan(int64_t T, int64_t H, int A, int per, int K, int weights, boo
 template <int DT, int WT>
 cudaError_t norm_forward_ring(const NormArgs& a, cudaStream_t s, bool* done) {
   constexpr int VE = Elem<DT>::kVec, N = 16 / VE;
-  const bool wide = (a.H + 2 * VE - 2) / VE > 512 * N;
-  const RingPlan p = ring_plan<VE>(a.T, a.H, 1, wide ? 2 * N : N, 2, 2, false, false);
+  const bool wide = (a.H + 2 * VE - 2) / VE > kRingThreads * N;
+  const RingPlan p = ring_plan<VE>(a.T, a.H, 1, wide ? 2 * N : N, 2, 2, false, false, 2);
   auto k = wide ? norm_ring_kernel<DT, WT, 2 * N, 2> : norm_ring_kernel<DT, WT, N, 2>;
   *done = p.ok && ensure_smem_limit(reinterpret_cast<const void*>(k), static_cast<int>(p.smem));
   if (!*done) return cudaSuccess;
@@ -1178,13 +1214,13 @@ int norm_backward_ring(const NormBwdArgs& a, cudaStream_t s, cudaError_t* e) {
   constexpr int VE = Elem<DT>::kVec, N = 16 / VE;  // windows of a thread that holds 16 columns
   constexpr int K = VE == 8 ? 2 : 1;
   const int n = static_cast<int>(kAligned ? a.H / VE : (static_cast<int64_t>(a.H) + 2 * VE - 2) / VE);
-  const bool hold = n <= 512 * N;
-  const int per = !hold ? 2 * N : n <= 32 ? 1 : N;
-  const RingPlan p = ring_plan<VE>(a.T, a.H, 2, per, hold ? K : 1, 1, kAligned, true);
+  const bool hold = n <= kRingThreads * N;
+  const int per = hold ? N : 2 * N;
+  const RingPlan p = ring_plan<VE>(a.T, a.H, 2, per, hold ? K : 1, hold ? 0 : 1, kAligned, true,
+                                   kAligned || hold ? 2 : 3);
   if (!p.ok) return 0;
-  auto k = !hold      ? norm_bwd_ring_kernel<DT, WT, 2 * N, 1, false, kAligned>
-           : per == 1 ? norm_bwd_ring_kernel<DT, WT, 1, K, true, kAligned>
-                      : norm_bwd_ring_kernel<DT, WT, N, K, true, kAligned>;
+  auto k = hold ? norm_bwd_ring_kernel<DT, WT, N, K, true, kAligned>
+                : norm_bwd_ring_kernel<DT, WT, 2 * N, 1, false, kAligned>;
   if (!ensure_smem_limit(reinterpret_cast<const void*>(k), static_cast<int>(p.smem))) return 0;
   *e = launch_pdl(k, dim3(p.grid), dim3(p.G * p.R), p.smem, s, a, p.G, p.R, p.S, p.C);
   note_launches(1);

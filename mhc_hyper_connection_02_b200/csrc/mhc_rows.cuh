@@ -170,6 +170,19 @@ __device__ __forceinline__ uint4 load_window(const typename Elem<DT>::raw* row, 
   return w;
 }
 
+// ------------------------------------------------------------------------------ async copies
+
+// Four bytes global -> shared without a register; async_copies_arrive lets `bar` count one arrival
+// once this thread's copies so far are there (an arrival its initial count includes).
+__device__ __forceinline__ void async_copy4(void* smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem)), "l"(gmem)
+               : "memory");
+}
+__device__ __forceinline__ void async_copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
 // ------------------------------------------------------------------------------ pairs
 //
 // Two fp32 operations in one instruction (each rounded as on its own): half the issue slots where
