@@ -353,6 +353,8 @@ struct RowRing {
   uint32_t first, step;  // in the class: the group's first, and from one stage to its next
   int H, classes, cls;
   int slot;           // windows of a row in a stage
+  int n;              // windows of an output row
+  uint4* masks;       // of the first and of the last one: the row's elements
   uint8_t* stages;
   uint64_t* full;
   float* stats;       // per stage: K pairs of mean and rstd (A = 2)
@@ -395,6 +397,17 @@ struct RowRing {
     off[i] = kAligned ? 0 : window_offset<DT>(base[i]);
     shift[i] = off[i] - out_off;
   }
+  // The output's windows, for phase out_off; by all threads, before the CTA's next barrier.
+  __device__ __forceinline__ void output(int out_off, uint4* two_masks) {
+    n = kAligned ? H / VE : window_count<DT>(out_off, H);
+    masks = two_masks;
+    if (!kAligned && threadIdx.x < 2 * VE) {
+      const int which = threadIdx.x / VE, q = threadIdx.x % VE;
+      const int e = (which == 0 ? 0 : n - 1) * VE - out_off + q;
+      reinterpret_cast<typename std::conditional<DT == 2, uint32_t, raw>::type*>(masks)[threadIdx.x] =
+          e >= 0 && e < H ? ~0u : 0u;
+    }
+  }
   __device__ __forceinline__ int64_t token(uint32_t j) const {
     return cls + static_cast<int64_t>(j) * classes;
   }
@@ -407,45 +420,26 @@ struct RowRing {
            (r * A + i) * slot;
   }
 
-  // Windows [from, to) of token t's row that are copied, and (unaligned) the elements that are not.
-  __device__ __forceinline__ int2 copied(int i, int64_t t) const {
-    const int end = off[i] + H;
-    return make_int2(t == 0 && off[i] > 0 ? 1 : 0,
-                     t == tokens - 1 ? end / VE : (end + VE - 1) / VE);
-  }
   // Starts the copy of the tokens j .. into a stage (one thread). A stage that the class's last
   // token does not fill gets that token again.
   __device__ __forceinline__ void copy(int st, uint32_t j) const {
-    uint32_t bytes = A * K * (H / VE) * 16;
-    if constexpr (!kAligned) {
-      bytes = 0;
+    // Rows where an array begins or ends: at either end of the class at most.
+    if (!kAligned && (j == 0 || j + K >= T) &&
+        (token(j) == 0 || token(min(j + K - 1, T - 1)) == tokens - 1)) {
+      copy_ends(st, j);
+    } else {
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int i = 0; i < A; ++i) bytes += windows(i);
+      mbar_arrive_expect_tx(&full[st], bytes * (K * 16));
+#pragma unroll
       for (int r = 0; r < K; ++r)
 #pragma unroll
-        for (int i = 0; i < A; ++i) {
-          const int2 w = copied(i, token(min(j + r, T - 1)));
-          bytes += (w.y - w.x) * 16;
-        }
+        for (int i = 0; i < A; ++i)
+          bulk_g2s(slot_at(st, r, i) + (kAligned ? 0 : 1),
+                   base[i] - off[i] + static_cast<int64_t>(min(j + r, T - 1)) * stride[i],
+                   windows(i) * 16, &full[st]);
     }
-    mbar_arrive_expect_tx(&full[st], bytes);
-#pragma unroll
-    for (int r = 0; r < K; ++r)
-#pragma unroll
-      for (int i = 0; i < A; ++i) {
-        const uint32_t at = min(j + r, T - 1);
-        const raw* row = base[i] + static_cast<int64_t>(at) * stride[i];
-        uint4* to = slot_at(st, r, i);
-        if constexpr (kAligned) {
-          bulk_g2s(to, row, H / VE * 16, &full[st]);
-        } else {
-          const int2 w = copied(i, token(at));
-          ++to;
-          raw* elements = reinterpret_cast<raw*>(to) + off[i];
-          if (w.x > 0)
-            for (int e = 0; e < VE - off[i]; ++e) elements[e] = row[e];
-          for (int e = w.y * VE - off[i]; e < H; ++e) elements[e] = row[e];
-          bulk_g2s(to + w.x, row - off[i] + w.x * VE, (w.y - w.x) * 16, &full[st]);
-        }
-      }
     if constexpr (A == 2) {
 #pragma unroll
       for (int r = 0; r < K; ++r) {
@@ -456,13 +450,39 @@ struct RowRing {
       async_copies_arrive(&full[st]);
     }
   }
+  __device__ __forceinline__ int windows(int i) const {
+    return kAligned ? H / VE : (off[i] + H + VE - 1) / VE;
+  }
+  // The same with rows that an array begins or ends with: only the windows that such a row fills.
+  __device__ __noinline__ void copy_ends(int st, uint32_t j) const {
+    for (int turn = 0; turn < 2; ++turn) {  // the sum of bytes, then the copies
+      uint32_t bytes = 0;
+      for (int r = 0; r < K; ++r)
+        for (int i = 0; i < A; ++i) {
+          const uint32_t at = min(j + r, T - 1);
+          const raw* row = base[i] + static_cast<int64_t>(at) * stride[i];
+          const int64_t t = token(at);
+          const int from = t == 0 && off[i] > 0 ? 1 : 0;
+          const int to = t == tokens - 1 ? (off[i] + H) / VE : windows(i);
+          bytes += (to - from) * 16;
+          if (turn == 0) continue;
+          uint4* slot_of = slot_at(st, r, i) + 1;
+          raw* elements = reinterpret_cast<raw*>(slot_of) + off[i];
+          if (from > 0)
+            for (int e = 0; e < VE - off[i]; ++e) elements[e] = row[e];
+          for (int e = to * VE - off[i]; e < H; ++e) elements[e] = row[e];
+          bulk_g2s(slot_of + from, row - off[i] + from * VE, (to - from) * 16, &full[st]);
+        }
+      if (turn == 0) mbar_arrive_expect_tx(&full[st], bytes);
+    }
+  }
   // The first S stages.
   __device__ __forceinline__ void start() const {
     for (int i = 0; i < S && first + i * step < T; ++i) copy(i, first + i * step);
   }
 
   // Output window s of row r of array i; what lies outside the row comes back as zero.
-  __device__ __forceinline__ uint4 window(int st, int r, int i, int s, int out_off) const {
+  __device__ __forceinline__ uint4 window(int st, int r, int i, int s) const {
     const uint4* p = slot_at(st, r, i) + s;
     if constexpr (kAligned) {
       return *p;
@@ -485,17 +505,9 @@ struct RowRing {
         w = make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
                        __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits));
       }
-      const int e0 = s * VE - out_off;
-      if (e0 < 0 || e0 + VE > H) {
-        uint32_t* words = &w.x;
-#pragma unroll
-        for (int q = 0; q < VE; ++q)
-          if (e0 + q < 0 || e0 + q >= H) {
-            if constexpr (DT == 2)
-              words[q] = 0;
-            else
-              words[q / 2] &= q % 2 ? 0x0000ffffu : 0xffff0000u;
-          }
+      if (s == 0 || s == n - 1) {
+        const uint4 m = masks[s == 0 ? 0 : 1];
+        w = make_uint4(w.x & m.x, w.y & m.y, w.z & m.z, w.w & m.w);
       }
       return w;
     }
@@ -546,23 +558,40 @@ __device__ __forceinline__ void unpack_pairs(const uint4& w, F2 (&v)[Elem<DT>::k
 #pragma unroll
   for (int q = 0; q < Elem<DT>::kVec / 2; ++q) v[q] = f2(f[2 * q], f[2 * q + 1]);
 }
-// Windows' output: whole ones at once, the elements of those at a row's ends one by one.
+// Windows' output: whole ones at once; of those at a row's ends the elements in the row, which end
+// or begin with the window, in at most three parts of 1, 2 and 4 elements.
 template <int DT, bool kAligned>
 __device__ __forceinline__ void put_window(typename Elem<DT>::raw* row, int H, int e0,
                                            const F2 (&v)[Elem<DT>::kVec / 2]) {
   using E = Elem<DT>;
-  float o[E::kVec];
+  using raw = typename E::raw;
+  constexpr int VE = E::kVec;
+  float o[VE];
 #pragma unroll
-  for (int q = 0; q < E::kVec / 2; ++q) {
+  for (int q = 0; q < VE / 2; ++q) {
     const float2 u = split(v[q]);
     o[2 * q] = u.x, o[2 * q + 1] = u.y;
   }
-  if (kAligned || (e0 >= 0 && e0 + E::kVec <= H)) {
-    st_stream(row + e0, E::pack(o));
-  } else {
+  const uint4 w = E::pack(o);
+  raw* const to = row + e0;
+  if (kAligned || (e0 >= 0 && e0 + VE <= H)) {
+    st_stream(to, w);
+  } else if constexpr (DT == 2) {
+    const uint32_t f[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int q = 0; q < E::kVec; ++q)
-      if (e0 + q >= 0 && e0 + q < H) row[e0 + q] = E::from_f32(o[q]);
+    for (int q = 0; q < 4; ++q)
+      if (e0 + q >= 0 && e0 + q < H) to[q] = __uint_as_float(f[q]);
+  } else if (e0 < 0) {  // the last c elements of the window
+    const int c = VE + e0;
+    if (c & 1) to[VE - c] = static_cast<raw>((c & 4 ? (c & 2 ? w.x : w.y) : (c & 2 ? w.z : w.w)) >> 16);
+    if (c & 2) *reinterpret_cast<uint32_t*>(to + (c & 4 ? 2 : 6)) = c & 4 ? w.y : w.w;
+    if (c & 4) *reinterpret_cast<uint2*>(to + 4) = make_uint2(w.z, w.w);
+  } else {  // the first c
+    const int c = H - e0;
+    if (c & 4) *reinterpret_cast<uint2*>(to) = make_uint2(w.x, w.y);
+    if (c & 2) *reinterpret_cast<uint32_t*>(to + (c & 4)) = c & 4 ? w.z : w.x;
+    if (c & 1)
+      to[c - 1] = static_cast<raw>((c & 4 ? (c & 2 ? w.w : w.z) : (c & 2 ? w.y : w.x)) & 0xffffu);
   }
 }
 
@@ -582,12 +611,15 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
   __shared__ float red[2][2 * 32];
   const int warp = threadIdx.x >> 5;
   const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
+  __shared__ uint4 masks[2];
   using Ring = RowRing<DT, 1, K, false>;
   if (threadIdx.x == 0) Ring::init_barriers(full, R * S);
   Ring rr;
   rr.init(a.T, a.H, C, R, group, S, ring, full);
   raw* const y0 = static_cast<raw*>(a.y) + static_cast<int64_t>(rr.cls) * a.H;
-  const int off = window_offset<DT>(y0), n = window_count<DT>(off, a.H);
+  const int off = window_offset<DT>(y0);
+  rr.output(off, masks);
+  const int n = rr.n;
   rr.array(0, a.x, a.x_stride, off);
   float* const gs = reinterpret_cast<float*>(ring + static_cast<size_t>(R * S) * rr.stage_bytes());
   float* const bs = gs + n * VE;
@@ -632,7 +664,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int at = i * G + tid;
-        h[r][i] = at < n ? rr.window(st, r, 0, at, off) : make_uint4(0, 0, 0, 0);
+        h[r][i] = at < n ? rr.window(st, r, 0, at) : make_uint4(0, 0, 0, 0);
         F2 x[P];
         unpack_pairs<DT>(h[r][i], x);
 #pragma unroll
@@ -728,13 +760,15 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
   const int warp = threadIdx.x >> 5;
   const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
   __shared__ __align__(8) float stats[kRingStages * 2 * K];
+  __shared__ uint4 masks[2];
   using Ring = RowRing<DT, 2, K, kAligned>;
   if (threadIdx.x == 0) Ring::init_barriers(full, R * S);
   Ring rr;
   rr.init(a.T, a.H, C, R, group, S, ring, full, stats, a.mean, a.rstd);
   raw* const dx0 = static_cast<raw*>(a.dx) + static_cast<int64_t>(rr.cls) * a.H;
   const int off = kAligned ? 0 : window_offset<DT>(dx0);
-  const int n = kAligned ? a.H / VE : window_count<DT>(off, a.H);
+  rr.output(off, masks);
+  const int n = rr.n;
   rr.array(0, a.x, a.x_stride, off);
   rr.array(1, a.dy, a.dy_stride, off);
   pdl_wait();
@@ -742,18 +776,19 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
   __syncthreads();
   const int nw = G >> 5, w0 = group * nw;
   if (tid == 0) rr.start();
-  // gamma: in registers (kHold), or behind the stages.
+  // gamma: in registers, where they have room for it, or behind the stages.
+  constexpr bool kOwn = kHold && kAligned;
   const auto* const gamma = static_cast<const typename W::raw*>(a.gamma);
   float* const gs = reinterpret_cast<float*>(ring + static_cast<size_t>(R * S) * rr.stage_bytes());
-  [[maybe_unused]] F2 own[kHold ? N : 1][P];
-  if constexpr (kHold) {
+  [[maybe_unused]] F2 own[kOwn ? N : 1][P];
+  if constexpr (kOwn) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float v[VE];
 #pragma unroll
       for (int q = 0; q < VE; ++q) {
-        const int h = (i * G + tid) * VE - off + q;
-        v[q] = h < 0 || h >= a.H ? 0.0f : gamma ? W::to_f32(__ldg(gamma + h)) : 1.0f;
+        const int h = (i * G + tid) * VE + q;
+        v[q] = h >= a.H ? 0.0f : gamma ? W::to_f32(__ldg(gamma + h)) : 1.0f;
       }
 #pragma unroll
       for (int q = 0; q < P; ++q) own[i][q] = f2(v[2 * q], v[2 * q + 1]);
@@ -762,7 +797,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
     stage_weights<VE, W>(gs, gamma, 1.0f, a.H, off, n);
   }
   auto weights = [&](int i, int at, F2 (&g)[P]) {
-    if constexpr (kHold) {
+    if constexpr (kOwn) {
 #pragma unroll
       for (int q = 0; q < P; ++q) g[q] = own[i][q];
     } else {
@@ -805,8 +840,8 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
         for (int i = 0; i < N; ++i) {
           const int at = i * G + tid;
           if (at < n) {
-            hx[r][i] = rr.window(st, r, 0, at, off);
-            hd[r][i] = rr.window(st, r, 1, at, off);
+            hx[r][i] = rr.window(st, r, 0, at);
+            hd[r][i] = rr.window(st, r, 1, at);
             if (r > 0 && !whole) hx[r][i] = hd[r][i] = make_uint4(0, 0, 0, 0);
           }
         }
@@ -823,8 +858,8 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
 #pragma unroll
         for (int r = 0; r < K; ++r) {
           F2 x[P], d[P];
-          unpack_pairs<DT>(kHold ? hx[r][i] : rr.window(st, r, 0, at, off), x);
-          unpack_pairs<DT>(kHold ? hd[r][i] : rr.window(st, r, 1, at, off), d);
+          unpack_pairs<DT>(kHold ? hx[r][i] : rr.window(st, r, 0, at), x);
+          unpack_pairs<DT>(kHold ? hd[r][i] : rr.window(st, r, 1, at), d);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             const F2 u = d[q] * (x[q] + nm[r]);
@@ -877,8 +912,8 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
         for (int r = 0; r < K; ++r) {
           if (r > 0 && !whole) break;
           F2 x[P], d[P];
-          unpack_pairs<DT>(kHold ? hx[r][i] : rr.window(st, r, 0, at, off), x);
-          unpack_pairs<DT>(kHold ? hd[r][i] : rr.window(st, r, 1, at, off), d);
+          unpack_pairs<DT>(kHold ? hx[r][i] : rr.window(st, r, 0, at), x);
+          unpack_pairs<DT>(kHold ? hd[r][i] : rr.window(st, r, 1, at), d);
 #pragma unroll
           for (int q = 0; q < P; ++q)
             x[q] = fma2(d[q] * g[q], fr[r], fma2(x[q], fx[r], f0[r]));
@@ -1216,7 +1251,8 @@ int norm_backward_ring(const NormBwdArgs& a, cudaStream_t s, cudaError_t* e) {
   const int n = static_cast<int>(kAligned ? a.H / VE : (static_cast<int64_t>(a.H) + 2 * VE - 2) / VE);
   const bool hold = n <= kRingThreads * N;
   const int per = hold ? N : 2 * N;
-  const RingPlan p = ring_plan<VE>(a.T, a.H, 2, per, hold ? K : 1, hold ? 0 : 1, kAligned, true,
+  const RingPlan p = ring_plan<VE>(a.T, a.H, 2, per, hold ? K : 1, hold && kAligned ? 0 : 1,
+                                   kAligned, true,
                                    kAligned || hold ? 2 : 3);
   if (!p.ok) return 0;
   auto k = hold ? norm_bwd_ring_kernel<DT, WT, N, K, true, kAligned>
