@@ -199,7 +199,7 @@ def _check(st: int, what: str) -> None:
 
 
 def _ptr(t) -> int:
-    return 0 if t is None else int(t.data_ptr())
+    return 0 if t is None else t.data_ptr()
 
 
 def _stream(stream):
@@ -510,14 +510,24 @@ def sinkhorn(logits, *, comb=None, iters: int = 20, eps: float = 1e-6, stream=No
     return comb
 
 
+# The row operators. Their GPU time at one token is a few microseconds, less than a careless wrapper
+# takes on the host: checks run once on what the caller gave and not on what is allocated here, and
+# the device's current stream is read as a handle.
+
+_codes: dict = {}
+
+
 def _dtype(t, name):
     import torch
-    code = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+    if not _codes:
+        _codes.update({torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16,
+                       torch.float32: DTYPE_F32})
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in code:
+    code = _codes.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} must be bfloat16, float16 or float32 (got {t.dtype})")
-    return code[t.dtype]
+    return code
 
 
 def _rows(t, name, shape=None, dtype=None, device=None):
@@ -529,8 +539,10 @@ def _rows(t, name, shape=None, dtype=None, device=None):
     T, N = t.shape
     if N < 1:
         raise ValueError(f"{name} must have at least one column")
-    stride = t.stride(0) if T > 1 else N
-    if (N > 1 and t.stride(1) != 1) or stride < N:
+    stride, inner = t.stride()
+    if T <= 1:
+        stride = N
+    if (N > 1 and inner != 1) or stride < N:
         raise ValueError(f"{name}: the elements of a row must be contiguous and rows must not "
                          f"overlap (strides {tuple(t.stride())})")
     if shape is not None and (T, N) != tuple(shape):
@@ -542,23 +554,20 @@ def _rows(t, name, shape=None, dtype=None, device=None):
     return stride
 
 
-class _Launch:
-    """The stream of a call on `device`: the given one (a torch stream or a handle), else the
-    device's current one. While it is entered, allocations belong to that stream; at the end the
-    tensors of the call are marked as used there, so that memory freed on their own stream is not
-    handed out again too early."""
+class _OtherStream:
+    """A call on a given stream (a torch stream or a handle). While it is entered, allocations
+    belong to that stream; at the end the tensors of the call are marked as used there, so that
+    memory freed on their own stream is not handed out again too early."""
 
-    def __init__(self, stream, device, *tensors):
+    def __init__(self, stream, device, tensors):
         import torch
         current = torch.cuda.current_stream(device)
-        if stream is None:
-            stream = current
-        elif not isinstance(stream, torch.cuda.Stream):
+        if not isinstance(stream, torch.cuda.Stream):
             stream = current if int(stream) == current.cuda_stream else \
                 torch.cuda.ExternalStream(int(stream), device=device)
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-        self.handle = ctypes.c_void_p(int(stream.cuda_stream))
+        self.handle = int(stream.cuda_stream)
         self._other = stream if stream.cuda_stream != current.cuda_stream else None
         self._tensors = tensors
         self._scope = torch.cuda.stream(stream) if self._other is not None else None
@@ -566,7 +575,7 @@ class _Launch:
     def __enter__(self):
         if self._scope is not None:
             self._scope.__enter__()
-        return self
+        return self.handle
 
     def __exit__(self, *exc):
         if self._scope is not None:
@@ -577,20 +586,47 @@ class _Launch:
         return False
 
 
+class _CurrentStream:
+    """A call on the device's current stream."""
+
+    def __init__(self, device):
+        import torch
+        self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        return False
+
+
+def _launch(stream, device, *tensors):
+    """The stream of a call on `device`: the given one, else the device's current one."""
+    if stream is None:
+        return _CurrentStream(device)
+    return _OtherStream(stream, device, tensors)
+
+
 def _need_on(t, dtype, shape, name, device):
+    try:  # what a right argument passes
+        if t.dtype is dtype and t.device == device and t.is_cuda and t.is_contiguous() and \
+                (shape is None or t.shape == shape):
+            return
+    except AttributeError:
+        pass
     _need(t, dtype, shape, name)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _norm_weight(t, name, x):
-    import torch
     if t is None:
         return None
     code = _dtype(t, name)
-    if t.dtype not in (torch.float32, x.dtype):
-        raise ValueError(f"{name} must be float32 or of the rows' type {x.dtype} (got {t.dtype})")
-    _need_on(t, t.dtype, (x.shape[1],), name, x.device)
+    dtype = t.dtype
+    if code != DTYPE_F32 and dtype != x.dtype:
+        raise ValueError(f"{name} must be float32 or of the rows' type {x.dtype} (got {dtype})")
+    _need_on(t, dtype, x.shape[1:], name, x.device)
     return code
 
 
@@ -607,16 +643,22 @@ def layer_norm(x, gamma=None, beta=None, *, eps: float = 1e-6, y=None, mean=None
     bd = _norm_weight(beta, "beta", x)
     if wd is not None and bd is not None and wd != bd:
         raise ValueError("gamma and beta must be of one type")
-    with _Launch(stream, dev, x, gamma, beta, y, mean, rstd) as on:
-        y = torch.empty((T, H), dtype=x.dtype, device=dev) if y is None else y
-        mean = torch.empty(T, dtype=torch.float32, device=dev) if mean is None else mean
-        rstd = torch.empty(T, dtype=torch.float32, device=dev) if rstd is None else rstd
+    if y is not None:
         _need_on(y, x.dtype, (T, H), "y", dev)
+    if mean is not None:
         _need_on(mean, torch.float32, (T,), "mean", dev)
+    if rstd is not None:
         _need_on(rstd, torch.float32, (T,), "rstd", dev)
-        st = lib().mhc_layer_norm(_ptr(x), stride, _dtype(x, "x"), _ptr(gamma), _ptr(beta),
+    with _launch(stream, dev, x, gamma, beta, y, mean, rstd) as handle:
+        if y is None:
+            y = x.new_empty((T, H))
+        if mean is None:
+            mean = x.new_empty(T, dtype=torch.float32)
+        if rstd is None:
+            rstd = mean.new_empty(T)
+        st = lib().mhc_layer_norm(_ptr(x), stride, _codes[x.dtype], _ptr(gamma), _ptr(beta),
                                   wd if wd is not None else bd if bd is not None else DTYPE_F32,
-                                  _ptr(y), _ptr(mean), _ptr(rstd), T, H, float(eps), on.handle)
+                                  _ptr(y), _ptr(mean), _ptr(rstd), T, H, float(eps), handle)
     _check(st, "mhc_layer_norm")
     return y, mean, rstd
 
@@ -636,23 +678,33 @@ def layer_norm_backward(d_y, x, gamma, mean, rstd, *, d_x=None, workspace=None, 
     wd = _norm_weight(gamma, "gamma", x)
     _need_on(mean, torch.float32, (T,), "mean", dev)
     _need_on(rstd, torch.float32, (T,), "rstd", dev)
-    with _Launch(stream, dev, d_y, x, gamma, mean, rstd, d_x, workspace) as on:
-        d_x = torch.empty((T, H), dtype=x.dtype, device=dev) if d_x is None else d_x
+    if d_x is not None:
         _need_on(d_x, x.dtype, (T, H), "d_x", dev)
-        d_gamma = torch.empty(H, dtype=torch.float32, device=dev)
-        d_beta = torch.empty(H, dtype=torch.float32, device=dev)
-        nws = layer_norm_backward_workspace_bytes(T, H)
-        if workspace is None and nws > 0:
-            workspace = torch.empty(nws, dtype=torch.uint8, device=dev)
-        if workspace is not None:
-            _need_on(workspace, workspace.dtype, None, "workspace", dev)
+    if workspace is not None:
+        _need_on(workspace, workspace.dtype, None, "workspace", dev)
+    with _launch(stream, dev, d_y, x, gamma, mean, rstd, d_x, workspace) as handle:
+        if d_x is None:
+            d_x = x.new_empty((T, H))
+        d_gamma = mean.new_empty(H)
+        d_beta = mean.new_empty(H)
+        if workspace is None and T > 0:
+            workspace = mean.new_empty(layer_norm_backward_workspace_bytes(T, H) // 4)
         wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
         st = lib().mhc_layer_norm_backward(
-            _ptr(d_y), ds, _ptr(x), xs, _dtype(x, "x"), _ptr(gamma),
+            _ptr(d_y), ds, _ptr(x), xs, _codes[x.dtype], _ptr(gamma),
             DTYPE_F32 if wd is None else wd, _ptr(mean), _ptr(rstd), _ptr(d_x), _ptr(d_gamma),
-            _ptr(d_beta), _ptr(workspace), wsb, T, H, on.handle)
+            _ptr(d_beta), _ptr(workspace), wsb, T, H, handle)
     _check(st, "mhc_layer_norm_backward")
     return d_x, d_gamma, d_beta
+
+
+def _grad_rows(logits, T, V, stride):
+    """An uninitialised gradient of the logits' type. Where the logits' rows are padded by less than
+    an eighth (a vocabulary rounded up for the product that made them), the gradient's are too: the
+    next product wants its rows aligned as well."""
+    if V < stride <= V + V // 8:
+        return logits.new_empty((T, stride))[:, :V]
+    return logits.new_empty((T, V))
 
 
 def token_logprobs(logits, targets=None, *, temperature: float = 1.0, top: int = 0,
@@ -670,16 +722,15 @@ def token_logprobs(logits, targets=None, *, temperature: float = 1.0, top: int =
         raise ValueError(f"top must be 0 to min(V, {TOP_MAX})")
     if targets is not None:
         _need_on(targets, torch.int64, (T,), "targets", dev)
-    with _Launch(stream, dev, logits, targets) as on:
-        f32 = dict(dtype=torch.float32, device=dev)
-        lp = torch.empty(T, **f32) if targets is not None else None
-        ent = torch.empty(T, **f32) if entropy else None
-        ti = torch.empty((T, top), dtype=torch.int64, device=dev) if top else None
-        tl = torch.empty((T, top), **f32) if top else None
-        stats = torch.empty((T, 2), **f32)
-        st = lib().mhc_token_logprobs(_ptr(logits), stride, _dtype(logits, "logits"),
-                                      _ptr(targets), float(temperature), _ptr(lp), _ptr(ent), top,
-                                      _ptr(ti), _ptr(tl), _ptr(stats), T, V, on.handle)
+    with _launch(stream, dev, logits, targets) as handle:
+        stats = logits.new_empty((T, 2), dtype=torch.float32)
+        lp = stats.new_empty(T) if targets is not None else None
+        ent = stats.new_empty(T) if entropy else None
+        ti = logits.new_empty((T, top), dtype=torch.int64) if top else None
+        tl = stats.new_empty((T, top)) if top else None
+        st = lib().mhc_token_logprobs(_ptr(logits), stride, _codes[logits.dtype], _ptr(targets),
+                                      float(temperature), _ptr(lp), _ptr(ent), top, _ptr(ti),
+                                      _ptr(tl), _ptr(stats), T, V, handle)
     _check(st, "mhc_token_logprobs")
     return lp, ent, ti, tl, stats
 
@@ -689,7 +740,8 @@ def token_logprobs_backward(logits, targets, stats, d_logprob=None, *, d_entropy
     """Gradient of token_logprobs' log probabilities and entropy to the logits, from the upstream
     gradients d_logprob [T] and d_entropy [T] (either may be None; entropy [T] goes with
     d_entropy) and the forward's stats. Returns d_logits [T,V] of the logits' type (pass
-    d_logits=logits to write it over them)."""
+    d_logits=logits to write it over them); its rows are as far apart as the logits' where those
+    are padded by less than an eighth of V, else dense."""
     import torch
     stride = _rows(logits, "logits")
     T, V = logits.shape
@@ -700,17 +752,26 @@ def token_logprobs_backward(logits, targets, stats, d_logprob=None, *, d_entropy
     for name, t in (("d_logprob", d_logprob), ("d_entropy", d_entropy), ("entropy", entropy)):
         if t is not None:
             _need_on(t, torch.float32, (T,), name, dev)
-    with _Launch(stream, dev, logits, targets, stats, d_logprob, d_entropy, entropy,
-                 d_logits) as on:
-        d_logits = torch.empty((T, V), dtype=logits.dtype, device=dev) if d_logits is None \
-            else d_logits
+    with _launch(stream, dev, logits, targets, stats, d_logprob, d_entropy, entropy,
+                 d_logits) as handle:
+        if d_logits is None:
+            d_logits = _grad_rows(logits, T, V, stride)
         ds = _rows(d_logits, "d_logits", (T, V), logits.dtype, dev)
         st = lib().mhc_token_logprobs_backward(
-            _ptr(logits), stride, _dtype(logits, "logits"), _ptr(targets), float(temperature),
+            _ptr(logits), stride, _codes[logits.dtype], _ptr(targets), float(temperature),
             _ptr(stats), _ptr(d_logprob), _ptr(d_entropy), _ptr(entropy), _ptr(d_logits), ds, T, V,
-            on.handle)
+            handle)
     _check(st, "mhc_token_logprobs_backward")
     return d_logits
+
+
+def _entries(index, T, device):
+    """K of the teacher's entries index [T,K]."""
+    import torch
+    _need_on(index, torch.int64, None, "index", device)
+    if index.dim() != 2 or index.shape[0] != T or not 1 <= index.shape[1] <= DISTILL_MAX:
+        raise ValueError(f"index must be [T, K] with 1 <= K <= {DISTILL_MAX}")
+    return index.shape[1]
 
 
 def distill_topk(logits, index, teacher, *, temperature: float = 1.0, stream=None):
@@ -721,19 +782,16 @@ def distill_topk(logits, index, teacher, *, temperature: float = 1.0, stream=Non
     stride = _rows(logits, "logits")
     T, V = logits.shape
     dev = logits.device
-    _need_on(index, torch.int64, None, "index", dev)
-    if index.dim() != 2 or index.shape[0] != T or not 1 <= index.shape[1] <= DISTILL_MAX:
-        raise ValueError(f"index must be [T, K] with 1 <= K <= {DISTILL_MAX}")
-    K = index.shape[1]
+    K = _entries(index, T, dev)
     td = _dtype(teacher, "teacher")
     _need_on(teacher, teacher.dtype, (T, K), "teacher", dev)
-    with _Launch(stream, dev, logits, index, teacher) as on:
-        f32 = dict(dtype=torch.float32, device=dev)
-        loss, weights = torch.empty(T, **f32), torch.empty((T, K), **f32)
-        stats = torch.empty((T, 2), **f32)
-        st = lib().mhc_distill_topk(_ptr(logits), stride, _dtype(logits, "logits"), _ptr(index),
+    with _launch(stream, dev, logits, index, teacher) as handle:
+        stats = logits.new_empty((T, 2), dtype=torch.float32)
+        loss = stats.new_empty(T)
+        weights = stats.new_empty((T, K))
+        st = lib().mhc_distill_topk(_ptr(logits), stride, _codes[logits.dtype], _ptr(index),
                                     _ptr(teacher), td, float(temperature), _ptr(loss),
-                                    _ptr(weights), _ptr(stats), T, V, K, on.handle)
+                                    _ptr(weights), _ptr(stats), T, V, K, handle)
     _check(st, "mhc_distill_topk")
     return loss, weights, stats
 
@@ -741,25 +799,23 @@ def distill_topk(logits, index, teacher, *, temperature: float = 1.0, stream=Non
 def distill_topk_backward(logits, index, weights, stats, d_loss, *, temperature: float = 1.0,
                           d_logits=None, stream=None):
     """Gradient of distill_topk's loss to the logits, from d_loss [T] and the forward's weights and
-    stats. Returns d_logits [T,V] of the logits' type (pass d_logits=logits to write over them)."""
+    stats. Returns d_logits [T,V] of the logits' type (pass d_logits=logits to write over them);
+    its rows are laid out as token_logprobs_backward's."""
     import torch
     stride = _rows(logits, "logits")
     T, V = logits.shape
     dev = logits.device
-    _need_on(index, torch.int64, None, "index", dev)
-    if index.dim() != 2 or index.shape[0] != T or not 1 <= index.shape[1] <= DISTILL_MAX:
-        raise ValueError(f"index must be [T, K] with 1 <= K <= {DISTILL_MAX}")
-    K = index.shape[1]
+    K = _entries(index, T, dev)
     _need_on(weights, torch.float32, (T, K), "weights", dev)
     _need_on(stats, torch.float32, (T, 2), "stats", dev)
     _need_on(d_loss, torch.float32, (T,), "d_loss", dev)
-    with _Launch(stream, dev, logits, index, weights, stats, d_loss, d_logits) as on:
-        d_logits = torch.empty((T, V), dtype=logits.dtype, device=dev) if d_logits is None \
-            else d_logits
+    with _launch(stream, dev, logits, index, weights, stats, d_loss, d_logits) as handle:
+        if d_logits is None:
+            d_logits = _grad_rows(logits, T, V, stride)
         ds = _rows(d_logits, "d_logits", (T, V), logits.dtype, dev)
         st = lib().mhc_distill_topk_backward(
-            _ptr(logits), stride, _dtype(logits, "logits"), _ptr(index), _ptr(weights),
-            _ptr(stats), _ptr(d_loss), float(temperature), _ptr(d_logits), ds, T, V, K, on.handle)
+            _ptr(logits), stride, _codes[logits.dtype], _ptr(index), _ptr(weights), _ptr(stats),
+            _ptr(d_loss), float(temperature), _ptr(d_logits), ds, T, V, K, handle)
     _check(st, "mhc_distill_topk_backward")
     return d_logits
 
