@@ -91,12 +91,18 @@ __device__ __forceinline__ RowPart row_part(const void* row, int n, int rank, in
 // element of bf16: the rest is therefore done on packed values (maximum, cut) and on pairs of fp32.
 // Without the pairs the entropy form took 406 us instead of the 352 us of the plain one (T=8192,
 // V=131072, bf16).
+// best: where this thread's maximum was met first, and the largest maximum of its other rounds.
+struct ThreadBest {
+  int round;     // first window of that round of kLgUnroll
+  float second;
+};
 template <int DT, int NT, bool kEnt>
 __device__ __forceinline__ RowSums thread_sums(const typename Elem<DT>::raw* row, const RowPart& p,
-                                               float c) {
+                                               float c, ThreadBest& best) {
   using E = Elem<DT>;
   constexpr int VE = E::kVec;
   RowSums r{-INFINITY, 0.f, 0.f};
+  best = {0, -INFINITY};
   F2 s2 = f2(0.f), u2 = f2(0.f);
   float mc = 0.f;
   const F2 c2 = f2(c);
@@ -110,7 +116,9 @@ __device__ __forceinline__ RowSums thread_sums(const typename Elem<DT>::raw* row
       w[j] = load_window<DT>(row, s < p.last ? p.n : 0, p.off, s);
     }
     const float tm = E::max_of(w);
+    best.second = fmaxf(best.second, fminf(tm, r.m));
     if (tm > r.m) {
+      best.round = s0;
       const float mcn = __fmul_rn(tm, c);
       float d = shift_of(r.m, tm, c);
       if (r.m != -INFINITY && small_mc(mc) && small_mc(mcn)) d = fmaxf(mc - mcn, -1000.0f);
@@ -235,10 +243,11 @@ struct TopShared {
   unsigned long long cand[kCand];
   unsigned long long list[kLgTopMax];
   unsigned long long warp_best[NT / 32];
-  uint32_t key[NT];
-  int holder[NT];
-  uint32_t threshold;
-  int count, holders;
+  // Maxima of groups of threads: enough that the K-th largest of them lets few elements through.
+  static constexpr int kGroup = NT >= 256 ? 4 : NT >= 128 ? 2 : 1, kGroups = NT / kGroup;
+  uint32_t key[kGroups];
+  int round[NT], thread[NT];
+  int count, rounds, threads;
   int scan[NT / 32];
 };
 
@@ -254,28 +263,38 @@ __device__ __forceinline__ void rank_select(TopShared<NT>& sh, int n, int K) {
   }
 }
 
-// Adds the elements with keys above `bar` (or at it, unless `above`) to the candidates. Only the
-// threads with a maximum that qualifies can hold such an element: their numbers are gathered, and
-// the whole CTA walks their windows, several at a time.
+// Adds the elements with keys from `least` on to the candidates. Only threads with a maximum that
+// qualifies can hold one, and all but those whose second round qualifies too in one round of windows
+// alone: the rounds and the threads are gathered, and the whole CTA walks them. Does nothing (returns
+// false) where more than `most` threads qualify.
 template <int DT, int NT>
-__device__ __forceinline__ void collect(const typename Elem<DT>::raw* row, const RowPart& p,
-                                        uint32_t own, uint32_t bar, bool above, TopShared<NT>& sh) {
+__device__ __forceinline__ bool collect(const typename Elem<DT>::raw* row, const RowPart& p,
+                                        uint32_t own, const ThreadBest& best, uint32_t least,
+                                        int most, TopShared<NT>& sh) {
   using E = Elem<DT>;
-  const uint32_t least = above ? bar + 1 : bar > 0 ? bar : 1;  // keys stay below 2^32 - 1
-  if (own >= least) sh.holder[atomicAdd(&sh.holders, 1)] = threadIdx.x;
+  if (own >= least) {
+    if (order_key(best.second) < least)
+      sh.round[atomicAdd(&sh.rounds, 1)] = best.round;
+    else
+      sh.thread[atomicAdd(&sh.threads, 1)] = p.first + threadIdx.x;
+  }
   __syncthreads();
-  const int holders = sh.holders, per = (p.last - p.first + NT - 1) / NT;
-  for (int i0 = threadIdx.x; i0 < holders * per; i0 += NT * kLgUnroll) {
-    uint4 w[kLgUnroll];
-    int at[kLgUnroll];
+  const int per = (p.last - p.first + NT - 1) / NT, rounds = kLgUnroll * sh.rounds;
+  const int items = rounds + sh.threads * per;
+  if (sh.rounds + sh.threads > most) return false;
+  for (int i0 = threadIdx.x; i0 < items; i0 += NT * 2) {
+    uint4 w[2];
+    int at[2];
 #pragma unroll
-    for (int j = 0; j < kLgUnroll; ++j) {
-      const int i = i0 + j * NT, h = i / per;
-      at[j] = i < holders * per ? p.first + sh.holder[h] + (i - h * per) * NT : p.last;
+    for (int j = 0; j < 2; ++j) {
+      const int i = i0 + j * NT, h = (i - rounds) / per;
+      at[j] = i < rounds  ? sh.round[i / kLgUnroll] + i % kLgUnroll * NT
+              : i < items ? sh.thread[h] + (i - rounds - h * per) * NT
+                          : p.last;
       w[j] = load_window<DT>(row, at[j] < p.last ? p.n : 0, p.off, at[j]);
     }
 #pragma unroll
-    for (int j = 0; j < kLgUnroll; ++j) {
+    for (int j = 0; j < 2; ++j) {
       if (at[j] >= p.last) continue;
       float x[E::kVec];
       E::unpack(w[j], x);
@@ -291,64 +310,71 @@ __device__ __forceinline__ void collect(const typename Elem<DT>::raw* row, const
     }
   }
   __syncthreads();
+  return true;
+}
+
+// The K-th largest of the groups' keys, in every lane of every warp; 0 when there are not as many.
+template <int DT, int NT>
+__device__ __forceinline__ uint32_t kth_key(const TopShared<NT>& sh, int K) {
+  constexpr int M = TopShared<NT>::kGroups / 32;
+  const int lane = threadIdx.x & 31;
+  uint32_t k[M], prefix = 0;
+#pragma unroll
+  for (int i = 0; i < M; ++i) k[i] = sh.key[i * 32 + lane];
+  for (int bit = 31; bit >= 32 - Elem<DT>::kOrderBits; --bit) {
+    const uint32_t trial = prefix | (1u << bit);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < M; ++i) n += __popc(__ballot_sync(0xffffffffu, k[i] >= trial));
+    if (n >= K) prefix = trial;
+    if (n == K) break;
+  }
+  uint32_t lowest = 0xffffffffu;
+#pragma unroll
+  for (int i = 0; i < M; ++i)
+    if (k[i] >= prefix && k[i] < lowest) lowest = k[i];
+  return __reduce_min_sync(0xffffffffu, lowest);
 }
 
 // The part's K best into sh.list, in order. `m` is this thread's maximum.
 //
-// The K-th largest of the threads' maxima bounds the K-th largest element from below, and only
+// The K-th largest of the thread groups' maxima bounds the K-th largest element from below, and only
 // threads whose maximum reaches it can hold an element that does: for logits in no special order
-// about K threads' windows are walked again, and a few more than K candidates are ranked. Where
-// many more threads (rows with long runs of one value: masked or constant rows) or more candidates
-// than fit reach the bound, those above it are taken first and the missing ones are the first
-// elements equal to it; where even those above it do not fit, K rounds each find the next best
+// a few more than K threads' windows are walked again, and a few more than K candidates are ranked.
+// Where many more threads (rows with long runs of one value: masked or constant rows) or more
+// candidates than fit reach the bound, those above it are taken first and the missing ones are the
+// first elements equal to it; where even those above it do not fit, K rounds each find the next best
 // element.
 template <int DT, int NT>
 __device__ __forceinline__ void top_of_part(const typename Elem<DT>::raw* row, const RowPart& p,
-                                            float m, int K, TopShared<NT>& sh) {
+                                            float m, const ThreadBest& best, int K,
+                                            TopShared<NT>& sh) {
   using E = Elem<DT>;
   constexpr int NW = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t own = p.first + tid < p.last ? order_key(m) : 0;
+  uint32_t of_group = own;
+#pragma unroll
+  for (int o = 1; o < TopShared<NT>::kGroup; o <<= 1)
+    of_group = max(of_group, __shfl_xor_sync(0xffffffffu, of_group, o));
   __syncthreads();
-  sh.key[tid] = own;
+  if (tid % TopShared<NT>::kGroup == 0) sh.key[tid / TopShared<NT>::kGroup] = of_group;
   if (tid < kLgTopMax) sh.list[tid] = 0;
-  if (tid == 0) sh.count = 0, sh.holders = 0;
+  if (tid == 0) sh.count = 0, sh.rounds = 0, sh.threads = 0;
   __syncthreads();
-  if (warp == 0) {
-    uint32_t k[NW], prefix = 0;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) k[i] = sh.key[i * 32 + lane];
-    for (int bit = 31; bit >= 32 - E::kOrderBits; --bit) {
-      const uint32_t trial = prefix | (1u << bit);
-      unsigned n = 0;
-#pragma unroll
-      for (int i = 0; i < NW; ++i) n += k[i] >= trial;
-      n = __reduce_add_sync(0xffffffffu, n);
-      if (n >= static_cast<unsigned>(K)) prefix = trial;
-      if (n == static_cast<unsigned>(K)) break;
-    }
-    uint32_t lowest = 0xffffffffu;
-#pragma unroll
-    for (int i = 0; i < NW; ++i)
-      if (k[i] >= prefix && k[i] < lowest) lowest = k[i];
-    lowest = __reduce_min_sync(0xffffffffu, lowest);
-    if (lane == 0) sh.threshold = lowest;
-  }
-  __syncthreads();
-  const uint32_t bar = sh.threshold;  // 0 when fewer than K threads hold elements
-  if (__syncthreads_count(own >= bar && own > 0) <= K + 32) {
-    collect<DT, NT>(row, p, own, bar, false, sh);
+  const uint32_t bar = kth_key<DT, NT>(sh, K);
+  if (collect<DT, NT>(row, p, own, best, bar > 0 ? bar : 1, 2 * K + 32, sh)) {
     const int n = sh.count;
     if (n <= TopShared<NT>::kCand) {
       rank_select<NT>(sh, n, K);
       __syncthreads();
       return;
     }
-    __syncthreads();
-    if (tid == 0) sh.count = 0, sh.holders = 0;
-    __syncthreads();
   }
-  collect<DT, NT>(row, p, own, bar, true, sh);
+  __syncthreads();
+  if (tid == 0) sh.count = 0, sh.rounds = 0, sh.threads = 0;
+  __syncthreads();
+  collect<DT, NT>(row, p, own, best, bar + 1, NT, sh);  // keys stay below 2^32 - 1
   const int n = sh.count;
   if (n <= TopShared<NT>::kCand) {
     rank_select<NT>(sh, n, K);
@@ -458,10 +484,11 @@ __global__ void __launch_bounds__(NT, logprob_ctas(NT, kTop)) logprob_kernel(con
   const int rank = static_cast<int>(blockIdx.x - t * a.ranks);
   const auto* row = static_cast<const typename E::raw*>(a.logits) + t * a.stride;
   const RowPart p = row_part<DT>(row, a.V, rank, a.ranks);
-  const RowSums own = thread_sums<DT, NT, kEnt>(row, p, a.c);
+  ThreadBest best;
+  const RowSums own = thread_sums<DT, NT, kEnt>(row, p, a.c, best);
   const RowSums mine = block_sums<NT, kEnt>(own, a.c, red);
   if (threadIdx.x == 0) part = mine;
-  if constexpr (kTop) top_of_part<DT, NT>(row, p, own.m, a.K, sh_top);
+  if constexpr (kTop) top_of_part<DT, NT>(row, p, own.m, best, a.K, sh_top);
   __syncthreads();
   if (a.ranks > 1) cooperative_groups::this_cluster().sync();
   if (rank == 0) {
@@ -536,7 +563,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a) {
   const int rank = static_cast<int>(blockIdx.x - t * a.ranks);
   const auto* row = static_cast<const typename E::raw*>(a.logits) + t * a.stride;
   const RowPart p = row_part<DT>(row, a.V, rank, a.ranks);
-  const RowSums mine = block_sums<NT, false>(thread_sums<DT, NT, false>(row, p, a.c), a.c, red);
+  ThreadBest best;
+  const RowSums mine = block_sums<NT, false>(thread_sums<DT, NT, false>(row, p, a.c, best), a.c, red);
   if (threadIdx.x == 0) part = mine;
   __syncthreads();
   if (a.ranks > 1) cooperative_groups::this_cluster().sync();
