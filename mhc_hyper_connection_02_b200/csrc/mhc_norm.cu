@@ -420,8 +420,9 @@ struct RowRing {
            (r * A + i) * slot;
   }
 
-  // Starts the copy of the tokens j .. into a stage (one thread). A stage that the class's last
-  // token does not fill gets that token again.
+  // Starts the copy of the tokens j .. into a stage (one thread; shared out over the group's warps it
+  // took 5 % longer), their statistics along with it. A stage that the class's last token does not
+  // fill gets that token again.
   __device__ __forceinline__ void copy(int st, uint32_t j) const {
     // Rows where an array begins or ends: at either end of the class at most.
     if (!kAligned && (j == 0 || j + K >= T) &&
@@ -893,14 +894,17 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
     if (G == 32) __syncwarp();
     if (tid == 0 && (kHold || lap + st > 0) && next < rr.T)
       rr.copy(kHold ? st : st > 0 ? st - 1 : S - 1, next);
-    // d_x = r d_y gamma - r c1 - (x - mean) r^2 c2 = r (d_y gamma) + (x f + f0). The mean's part of
-    // f0 is rounded against a product with c2, which is small where many columns make |mean| r large.
+    // d_x = r d_y gamma - r c1 - (x - mean) r^2 c2 = r (d_y gamma) + (x' f + f0). For 16-bit rows x' is
+    // x and the mean's part in f0: off by 2^-24 |mean| r of the last term, where a row of such a type
+    // has |mean| r below its own 2^8 or 2^11 steps. fp32 rows take x' = x - mean.
+    constexpr bool kFold = DT != 2;
     F2 f0[K], fx[K];
 #pragma unroll
     for (int r = 0; r < K; ++r) {
       const float f = -rs[r] * rs[r] * (rs[r] * sums[2 * r + 1] * per_h);
       fx[r] = f2(f);
-      f0[r] = f2(fmaf(split(nm[r]).x, f, -rs[r] * (sums[2 * r] * per_h)));
+      const float c = -rs[r] * (sums[2 * r] * per_h);
+      f0[r] = f2(kFold ? fmaf(split(nm[r]).x, f, c) : c);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -916,7 +920,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
           unpack_pairs<DT>(kHold ? hd[r][i] : rr.window(st, r, 1, at), d);
 #pragma unroll
           for (int q = 0; q < P; ++q)
-            x[q] = fma2(d[q] * g[q], fr[r], fma2(x[q], fx[r], f0[r]));
+            x[q] = fma2(d[q] * g[q], fr[r], fma2(kFold ? x[q] : x[q] + nm[r], fx[r], f0[r]));
           put_window<DT, kAligned>(dx + static_cast<int64_t>(r) * rr.classes * a.H, a.H,
                                    at * VE - off, x);
         }

@@ -61,9 +61,11 @@ def norm_bounds(x, gamma, beta, y, mean, rstd, eps):
     return ey, dm, rstd * rel
 
 
-def norm_bwd_bounds(d_y, x, gamma, mean, rstd):
+def norm_bwd_bounds(d_y, x, gamma, mean, rstd, dtype="fp32"):
     """Errors of (d_x before rounding, d_gamma, d_beta). Token sums: fewer than T / 64 + 96
-    additions in sequence where tokens are spread over 64 chains or more, and never above T."""
+    additions in sequence where tokens are spread over 64 chains or more, and never above T.
+    16-bit rows form (x - mean) f as x f + (c - mean f), f = r^2 c2 in size: the bracket and the sum
+    are rounded at the size of mean f, U each."""
     T, H = x.shape
     d = -(-H // 32) + 16
     r = rstd[:, None]
@@ -72,6 +74,8 @@ def norm_bwd_bounds(d_y, x, gamma, mean, rstd):
     c1, c2 = q.mean(1, keepdims=True), (q * xh).mean(1, keepdims=True)  # of sizes
     dc1, dc2 = (d + 4) * U * c1, (d + 8) * U * c2
     ex = r * (U * q + dc1 + xh * dc2 + 4 * U * xh * c2 + 4 * U * (q + c1 + xh * c2))
+    if dtype != "fp32":
+        ex = ex + 2 * U * r * (np.abs(mean)[:, None] * r) * c2
     n = min(T, -(-T // 64) + 96) + 4
     eg = (n + 4) * U * (np.abs(d_y) * xh).sum(0)
     eb = n * U * np.abs(d_y).sum(0)
@@ -80,16 +84,22 @@ def norm_bwd_bounds(d_y, x, gamma, mean, rstd):
 
 def row_sum_error(z, m, tau):
     """Relative error of s = sum exp((z - m) / tau), per row: E2 for each term and for each change
-    of a thread's running maximum (at most one per tile of 1024 16-byte windows, and three joins),
-    the additions, and U |d| in each exponent d (twice: its scale and its rounding)."""
+    of a thread's running maximum (at most one per round of windows, which are V / 4096 + 1 at most,
+    and three joins; 2 U for its factor and product), the additions, and U |d| in each exponent d
+    (twice: its scale and its rounding). Additions: a thread adds its elements two at a time. It has
+    at most 8 windows of 8 elements up to V = 2048 (32 threads), 16 windows up to V = 16384 (128
+    threads) and V / 256 + 8 elements beyond; then come one addition of the pair, five and seven over
+    the threads and seven over the CTAs of a row."""
     z = np.asarray(z, np.float64)
-    tiles = -(-z.shape[1] // 4096) + 3
+    V = z.shape[1]
+    tiles = -(-V // 4096) + 3
+    adds = (64 if V <= 2048 else 128 if V <= 16384 else V / 256 + 8) / 2 + 20
     base = np.where(np.isfinite(m), m, 0.0)[:, None]
     with np.errstate(invalid="ignore", over="ignore"):
         d = (z - base) / tau / LN2
         e = np.exp2(d)
         mean_d = np.where(e > 0, e * np.abs(d), 0).sum(1) / np.maximum(e.sum(1), 1e-300)
-    return (tiles + 2) * E2 + (4 * tiles + 24) * U + 2 * LN2 * U * (2 * mean_d + 1)
+    return (tiles + 2) * E2 + (2 * tiles + adds) * U + 2 * LN2 * U * (2 * mean_d + 1)
 
 
 def logprob_bounds(r, z, tau):

@@ -100,6 +100,36 @@ def test_top_alternatives(top, T, V):
     _check_forward(z, None, 1.0, top, mhc.token_logprobs(z, None, top=top))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("apart", [8, 256 * 8, 1024 * 4, 1024 * 8, 3 * 1024 * 8])
+def test_best_ones_at_one_distance(dtype, apart):
+    """The best elements lie `apart` elements from one another: in one window, one round or several
+    rounds of the same thread, equal ones among them."""
+    V = 70001
+    z = _logits(6, V, dtype, apart)
+    at = torch.arange(0, V, apart, device="cuda")[:40]
+    for t in range(6):
+        z[t, at + t] = (20 + torch.arange(at.numel(), device="cuda") % (3 + 7 * t)).to(z.dtype)
+    for top in (1, 9, 32):
+        _check_forward(z, None, 1.0, top, mhc.token_logprobs(z, None, top=top))
+
+
+def test_a_gradient_is_laid_out_as_padded_logits_are():
+    for V, stride, want in ((1000, 1024, 1024), (1001, 1008, 1008), (1000, 1000, 1000),
+                            (1000, 2000, 1000)):
+        z = torch.randn((5, stride), device="cuda").to(torch.bfloat16)[:, :V]
+        y, a = _targets(5, V, 1), torch.randn(5, device="cuda")
+        st = mhc.token_logprobs(z, y, entropy=False)[4]
+        d = mhc.token_logprobs_backward(z, y, st, a)
+        assert d.shape == (5, V) and d.stride() == (want, 1)
+        out = torch.empty((5, V), dtype=z.dtype, device="cuda")
+        mhc.token_logprobs_backward(z, y, st, a, d_logits=out)
+        assert torch.equal(out, d)
+        idx, t = _teacher(5, V, 4, "fp32", 1, ragged=False, twice=False)
+        loss, w, st = mhc.distill_topk(z, idx, t)
+        assert mhc.distill_topk_backward(z, idx, w, st, a).stride() == (want, 1)
+
+
 def _special_rows(V, dtype):
     """Rows that no-order-in-particular does not cover, for the top alternatives and the sums."""
     lowest = torch.finfo(DTYPES[dtype]).min

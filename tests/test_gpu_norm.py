@@ -39,7 +39,7 @@ def _check_forward(x, gamma, beta, got, dtype, eps=1e-6):
 def _check_backward(dy, x, gamma, mean, rstd, got, dtype):
     a = [f64(v) if v is not None else None for v in (dy, x, gamma, mean, rstd)]
     dx, dg, db = rows.layer_norm_backward(*a)
-    ex, eg, eb = norm_bwd_bounds(*a)
+    ex, eg, eb = norm_bwd_bounds(*a, dtype)
     check(got[0], dx, rounded(dx, ex, dtype), "d_x")
     check(got[1], dg, eg, "d_gamma")
     check(got[2], db, eb, "d_beta")
@@ -172,6 +172,66 @@ def test_gradient_against_differences():
     assert abs(diff - (dx.double() * v.double()).sum().item()) < 1e-3 * size
 
 
+def _rows_at(t, first, stride, fill):
+    """t's rows `stride` elements apart from element `first` of a buffer of `fill`, and the buffer."""
+    T, H = t.shape
+    buf = torch.full((first + (T - 1) * stride + H + 5,), fill, dtype=t.dtype, device="cuda")
+    rows_ = torch.as_strided(buf, (T, H), (stride, 1), first)
+    rows_.copy_(t)
+    return rows_, buf
+
+
+@pytest.mark.parametrize("T", [1, 2, 9, 331])
+@pytest.mark.parametrize("H", [1, 15, 16, 17, 33, 255, 1001, 5003])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_arrays_of_unlike_phases(T, H, dtype):
+    """x, d_y and the outputs begin at addresses and lie at distances of their own; what lies beside
+    the rows is a NaN that reaches nothing, and stays."""
+    x, dy, gamma, beta = _make(T, H, dtype, "fp32", T * H)
+    nan = float("nan")
+    for i, (fx, gx, fd, gd, fo) in enumerate([(0, 0, 0, 0, 0), (1, 0, 1, 0, 1), (3, 5, 0, 0, 2),
+                                             (2, H, 5, 3, 0), (0, 1, 7, 0, 3)]):
+        xs, bx = _rows_at(x, fx, H + gx, nan)
+        ds, bd = _rows_at(dy, fd, H + gd, nan)
+        out, bo = _rows_at(x, fo, H, nan)
+        keep = [b.clone() for b in (bx, bd)]
+        got = mhc.layer_norm(xs, gamma, beta, y=out)
+        edge = torch.cat((bo[:fo], bo[fo + T * H:]))
+        assert torch.isnan(edge).all() and edge.numel() == fo + 5
+        _check_forward(x, gamma, beta, got, dtype)
+        back = mhc.layer_norm_backward(ds, xs, gamma, got[1], got[2], d_x=out)
+        assert torch.isnan(torch.cat((bo[:fo], bo[fo + T * H:]))).all()
+        _check_backward(dy, x, gamma, got[1], got[2], back, dtype)
+        for b, k in zip((bx, bd), keep):
+            assert torch.equal(b.nan_to_num(7.0), k.nan_to_num(7.0))
+        if gx == 0:  # in place: the bits of an output of the same phase (the phase orders the sums)
+            ref = mhc.layer_norm(xs, gamma, beta, y=_rows_at(x, fx, H, nan)[0])[0]
+            assert torch.equal(mhc.layer_norm(xs, gamma, beta, y=xs)[0], ref)
+
+
+@pytest.mark.parametrize("T,H,dtype", [(310, 9001, "bf16"), (300, 14001, "fp16"),
+                                       (299, 16383, "bf16"), (305, 8190, "fp32"),
+                                       (300, 11000, "fp32"), (298, 8191, "fp32"),
+                                       (6000, 17, "bf16"), (5001, 100, "bf16")])
+def test_widths_at_the_forms_limits(T, H, dtype):
+    x, dy, gamma, beta = _make(T, H, dtype, "fp32", T + H, gap=1)
+    got = mhc.layer_norm(x, gamma, beta)
+    _check_forward(x, gamma, beta, got, dtype)
+    back = mhc.layer_norm_backward(dy, x, gamma, got[1], got[2])
+    _check_backward(dy, x, gamma, got[1], got[2], back, dtype)
+
+
+@pytest.mark.parametrize("H", [1000, 1001])
+def test_gradient_where_the_mean_is_far_above_the_deviation(H):
+    """fp32: x - mean is formed first."""
+    g = torch.Generator().manual_seed(H)
+    x = (1000 + torch.randn((300, H), generator=g)).cuda()
+    dy = torch.randn((300, H), generator=g).cuda()
+    _, mean, rstd = mhc.layer_norm(x)
+    _check_backward(dy, x, None, mean, rstd, mhc.layer_norm_backward(dy, x, None, mean, rstd),
+                    "fp32")
+
+
 @pytest.mark.slow
 def test_training_batch():
     """The training batch's size; all tokens' sums, sampled rows."""
@@ -183,7 +243,7 @@ def test_training_batch():
     _check_forward(x[pick], gamma, beta, (y[pick], mean[pick], rstd[pick]), "bf16")
     a = [f64(v) for v in (dy[pick], x[pick], gamma, mean[pick], rstd[pick])]
     rx, _, _ = rows.layer_norm_backward(*a)
-    check(dx[pick], rx, rounded(rx, norm_bwd_bounds(*a)[0], "bf16"), "d_x")
+    check(dx[pick], rx, rounded(rx, norm_bwd_bounds(*a, "bf16")[0], "bf16"), "d_x")
     tot = [0, 0, 0, 0]
     for i in range(0, T, 1024):  # the token sums, in chunks on the device in fp64
         s = slice(i, i + 1024)
