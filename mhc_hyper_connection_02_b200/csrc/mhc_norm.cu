@@ -614,6 +614,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
   const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
   __shared__ uint4 masks[2];
   using Ring = RowRing<DT, 1, K, false>;
+  __shared__ Ring plans[kRingThreads / 32];  // for the groups' copying threads: few registers
   if (threadIdx.x == 0) Ring::init_barriers(full, R * S);
   Ring rr;
   rr.init(a.T, a.H, C, R, group, S, ring, full);
@@ -622,13 +623,15 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
   rr.output(off, masks);
   const int n = rr.n;
   rr.array(0, a.x, a.x_stride, off);
+  Ring& plan = plans[group];
+  if (tid == 0) plan = rr;
   float* const gs = reinterpret_cast<float*>(ring + static_cast<size_t>(R * S) * rr.stage_bytes());
   float* const bs = gs + n * VE;
   pdl_wait();
   pdl_trigger();
   __syncthreads();
   const int nw = G >> 5, w0 = group * nw;
-  if (tid == 0) rr.start();
+  if (tid == 0) plan.start();
   stage_weights<VE, W>(gs, static_cast<const typename W::raw*>(a.gamma), 1.0f, a.H, off, n);
   stage_weights<VE, W>(bs, static_cast<const typename W::raw*>(a.beta), 0.0f, a.H, off, n);
   __syncthreads();
@@ -677,7 +680,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
     total(s, mean);
     if (!ok) break;
     if (G == 32) __syncwarp();
-    if (tid == 0 && j + S * rr.step < rr.T) rr.copy(st, j + S * rr.step);
+    if (tid == 0 && j + S * rr.step < rr.T) plan.copy(st, j + S * rr.step);
 #pragma unroll
     for (int r = 0; r < K; ++r) {
       mean[r] /= fh;
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
     }
     if (++st == S) st = 0, ++lap;
   }
-  if (!ok && tid == 0) rr.drain(st, lap, j, S);
+  if (!ok && tid == 0) plan.drain(st, lap, j, S);
 }
 
 // Backward. A group reads the rows of a stage once (kHold: they stay packed in its registers) or
@@ -763,6 +766,8 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
   __shared__ __align__(8) float stats[kRingStages * 2 * K];
   __shared__ uint4 masks[2];
   using Ring = RowRing<DT, 2, K, kAligned>;
+  // Unaligned, the groups' copying threads keep what they need here: few registers are free.
+  __shared__ Ring plans[kAligned ? 1 : kRingThreads / 32];
   if (threadIdx.x == 0) Ring::init_barriers(full, R * S);
   Ring rr;
   rr.init(a.T, a.H, C, R, group, S, ring, full, stats, a.mean, a.rstd);
@@ -772,11 +777,18 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
   const int n = rr.n;
   rr.array(0, a.x, a.x_stride, off);
   rr.array(1, a.dy, a.dy_stride, off);
+  if (!kAligned && tid == 0) plans[group] = rr;
+  auto plan = [&]() -> const Ring& {
+    if constexpr (kAligned)
+      return rr;
+    else
+      return plans[group];
+  };
   pdl_wait();
   pdl_trigger();
   __syncthreads();
   const int nw = G >> 5, w0 = group * nw;
-  if (tid == 0) rr.start();
+  if (tid == 0) plan().start();
   // gamma: in registers, where they have room for it, or behind the stages.
   constexpr bool kOwn = kHold && kAligned;
   const auto* const gamma = static_cast<const typename W::raw*>(a.gamma);
@@ -893,7 +905,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
     const uint32_t next = j + (S - lag) * rr.step;
     if (G == 32) __syncwarp();
     if (tid == 0 && (kHold || lap + st > 0) && next < rr.T)
-      rr.copy(kHold ? st : st > 0 ? st - 1 : S - 1, next);
+      plan().copy(kHold ? st : st > 0 ? st - 1 : S - 1, next);
     // d_x = r d_y gamma - r c1 - (x - mean) r^2 c2 = r (d_y gamma) + (x' f + f0). For 16-bit rows x' is
     // x and the mean's part in f0: off by 2^-24 |mean| r of the last term, where a row of such a type
     // has |mean| r below its own 2^8 or 2^11 steps. fp32 rows take x' = x - mean.
@@ -930,7 +942,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
     if (++st == S) st = 0, ++lap;
   }
   // Stages with a copy, from the current one on (the first pass of !kHold has them all).
-  if (!ok && tid == 0) rr.drain(st, lap, j, kHold || lap + st == 0 ? S : S - 1);
+  if (!ok && tid == 0) plan().drain(st, lap, j, kHold || lap + st == 0 ? S : S - 1);
   if (!a.part) return;
   // The groups' sums, through the stages' memory (free: every group is done).
   __syncthreads();
@@ -1186,7 +1198,7 @@ RingPlan ring_plan(int64_t T, int64_t H, int A, int per, int K, int weights, boo
   p.C = aligned ? 1 : VE;
   const size_t stage = static_cast<size_t>(A) * K * (aligned ? n : n + 2) * 16;
   const size_t w = static_cast<size_t>(weights) * n * VE * 4;  // staged weights
-  const size_t limit = 224 * 1024;
+  const size_t limit = (aligned ? 224 : 220) * 1024;  // beside the kernels' static 3 or 6 KB
   if (w >= limit) return p;
   const size_t fit = (limit - w) / (stage * p.R);
   const size_t most_stages = kRingStages / p.R < kStagesEach ? kRingStages / p.R : kStagesEach;
