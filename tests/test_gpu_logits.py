@@ -401,6 +401,34 @@ def test_same_bits_in_graphs_and_on_another_stream():
         assert torch.equal(v, w) and torch.equal(v2, w)
 
 
+@pytest.mark.parametrize("dtype,V", [("bf16", 66001), ("fp32", 33001)])
+def test_rows_left_over_after_full_rounds(dtype, V):
+    """As many rows as two launches share, between kernels that write the logits just before and
+    clear them just after."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    K = 12
+    for T in (sms * 5 + 9, sms * 6 + 9):
+        src, y = _logits(T, V, dtype, T), _targets(T, V, 2)
+        idx, t = _teacher(T, V, K, "fp32", 1)
+        z = torch.zeros_like(src)
+        pick = torch.tensor([0, 1, T // 2, *range(T - 12, T)], device="cuda")
+        zs, ys = src[pick], y[pick]
+        for top in (0, 6):
+            z.copy_(src)
+            got = mhc.token_logprobs(z, y, top=top)
+            z.zero_()
+            _check_forward(zs, ys, 1.0, top, [v if v is None else v[pick] for v in got])
+        z.copy_(src)
+        got = mhc.distill_topk(z, idx, t)
+        z.zero_()
+        _check_distill(zs, idx[pick], t[pick], 1.0, [v[pick] for v in got], dtype)
+        a = torch.randn(T, device="cuda")
+        z.copy_(src)
+        st = mhc.token_logprobs(z, y, entropy=False)[4]
+        d = mhc.token_logprobs_backward(z, y, st, a, d_logits=z)
+        _check_backward(zs, ys, 1.0, a[pick], None, st[pick], None, d[pick], dtype)
+
+
 def test_offsets_past_32_bits():
     """Rows whose byte and element offsets pass 2^31 and 2^32 (the last rows are checked)."""
     T, V = 3, 5000
