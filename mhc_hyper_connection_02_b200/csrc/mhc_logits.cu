@@ -1033,8 +1033,10 @@ int launch_distill(const DistillArgs& a, int64_t T, cudaStream_t s) {
 
 template <int DT>
 int launch_logit_grad(LogitGradArgs a, int64_t T, bool distill, cudaStream_t s) {
-  // Windows of a row at its worst alignment.
-  const int windows = (a.V + 2 * Elem<DT>::kVec - 2) / Elem<DT>::kVec;
+  // Windows of a row: one more than fill it where rows may begin anywhere in their first.
+  constexpr int VE = Elem<DT>::kVec;
+  const bool whole = aligned16(a.logits) && a.stride % VE == 0;
+  const int windows = (a.V + (whole ? VE - 1 : 2 * VE - 2)) / VE;
   const int threads = windows <= 256 ? 32 : windows <= 1024 ? 128 : 256;
   const int chunk = threads * kLgUnroll * kLgRounds;
   a.chunks = (windows + chunk - 1) / chunk;
