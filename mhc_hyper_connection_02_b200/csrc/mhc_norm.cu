@@ -62,12 +62,8 @@ struct Chunk {
   using E = Elem<DT>;
   using raw = typename E::raw;
   typename std::conditional<VW == 1, raw, uint4>::type v;
-  // kRo: not written by this kernel (read-only path). kKeep: worth keeping in L1 (weights).
   __device__ __forceinline__ void load(const raw* p) {
     if constexpr (VW == 1) v = *p; else v = ld_stream(p);
-  }
-  __device__ __forceinline__ void load_ro(const raw* p) {
-    if constexpr (VW == 1) v = __ldg(p); else v = ld_stream_ro(p);
   }
   __device__ __forceinline__ void get(float (&x)[VW]) const {
     if constexpr (VW == 1) x[0] = E::to_f32(v); else E::unpack(v, x);
@@ -235,92 +231,6 @@ __device__ __forceinline__ void add_groups(const float* sums, int R, int n, floa
     for (int j = 1; j < R; ++j) v += sums[static_cast<size_t>(j) * n + c];
     to[c] = v;
   }
-}
-
-// Backward for rows of any stride and alignment: d_x and the CTA's partial sums of the weights'
-// gradients in one pass over x and d_y, element by element. A CTA holds R groups of G threads; group
-// j of CTA i takes the tokens i R + j, + gridDim.x R, ..., and reads the next token's rows before it
-// exchanges sums for this one. Each thread keeps its N columns' gradient sums in registers; with one
-// column a thread (1024 threads a row) a row of 1001 took five times as long.
-template <int DT, int WT, int N>
-__global__ void __launch_bounds__(512) norm_bwd_row_kernel(const NormBwdArgs a, int G) {
-  using W = Elem<WT>;
-  using E = Elem<DT>;
-  using raw = typename E::raw;
-  extern __shared__ float group_sums[];  // [R][2][H] (R > 1)
-  __shared__ float red[2][2 * 32];       // by turn: each warp's sums (joined_sums)
-  pdl_wait();
-  pdl_trigger();
-  const int R = blockDim.x / G;
-  const int warp = threadIdx.x >> 5;
-  const int group = threadIdx.x / G, tid = threadIdx.x - group * G;
-  const int nw = G >> 5, w0 = group * nw;
-  const auto* gamma = static_cast<const typename W::raw*>(a.gamma);
-  const float fh = static_cast<float>(a.H);
-  float dg[N], db[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) dg[i] = db[i] = 0.0f;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * R;
-  int64_t t = blockIdx.x * static_cast<int64_t>(R) + group;
-  raw cx[N], cd[N];
-  float mean = 0.f, rstd = 0.f;
-  auto fetch = [&](int64_t at) {
-    const raw* x = static_cast<const raw*>(a.x) + at * a.x_stride;
-    const raw* dy = static_cast<const raw*>(a.dy) + at * a.dy_stride;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int h = i * G + tid;
-      if (h < a.H) cx[i] = __ldg(x + h), cd[i] = __ldg(dy + h);
-    }
-    mean = a.mean[at];
-    rstd = a.rstd[at];
-  };
-  if (t < a.T) fetch(t);
-  int turn = 0;
-  for (; t < a.T; t += step, turn ^= 1) {
-    float xh[N], q[N], sums[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int h = i * G + tid;
-      if (h < a.H) {
-        const float d = E::to_f32(cd[i]);
-        xh[i] = (E::to_f32(cx[i]) - mean) * rstd;
-        dg[i] = fmaf(d, xh[i], dg[i]);
-        db[i] += d;
-        q[i] = gamma ? d * W::to_f32(__ldg(gamma + h)) : d;
-        sums[0] += q[i];
-        sums[1] = fmaf(q[i], xh[i], sums[1]);
-      }
-    }
-    const float r = rstd;
-    if (t + step < a.T) fetch(t + step);
-    const float part = warp_sums<2>(sums);
-    if (G == 32) {
-      share_sums<2>(part, sums);
-    } else {
-      put_warp_sums<2>(part, red[turn], warp);
-      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(G) : "memory");
-      joined_sums<2>(red[turn], w0, nw, sums);
-    }
-    const float c1 = sums[0] / fh, c2 = sums[1] / fh;
-    raw* dx = static_cast<raw*>(a.dx) + t * a.H;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int h = i * G + tid;
-      if (h < a.H) dx[h] = E::from_f32(r * (q[i] - c1 - xh[i] * c2));
-    }
-  }
-  if (!a.part) return;
-  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
-  float* to = R > 1 ? group_sums + static_cast<size_t>(group) * 2 * a.H : part;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int h = i * G + tid;
-    if (h < a.H) to[h] = dg[i], to[a.H + h] = db[i];
-  }
-  if (R == 1) return;
-  __syncthreads();
-  add_groups(group_sums, R, 2 * a.H, part);
 }
 
 // ------------------------------------------------------------------------------ staged rows
@@ -599,7 +509,9 @@ __device__ __forceinline__ void put_window(typename Elem<DT>::raw* row, int H, i
 constexpr int kRingStages = 64;    // of all groups, at most
 constexpr int kRingThreads = 512;  // of all groups, at most
 
-// Forward of rows that are not whole windows. x is read once and stays packed in registers.
+// Forward of many rows that are not whole windows. x is read once and stays packed in registers.
+// T=8192, H=3501 bf16: 43 us (2.6 TB/s), element by element 80 us; bound by the instructions of a
+// group's warps, of which an SM holds 16.
 template <int DT, int WT, int N, int K>
 __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs a, int G, int R, int S,
                                                         int C) {
@@ -750,7 +662,12 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
 // Backward. A group reads the rows of a stage once (kHold: they stay packed in its registers) or
 // twice, and exchanges the sums of K tokens at once. Each thread keeps its columns' gradient sums in
 // registers over all its tokens: 16 columns at 512 threads an SM, which is what they and two held
-// rows leave room for. All waits are bounded, and a group leaves its loop together.
+// rows leave room for; with 8 columns at 1024 threads each warp's exchange costs as much for half the
+// work (T=8192, H=7168 bf16: 112 us instead of 67 us). All waits are bounded, and a group leaves its
+// loop together.
+//
+// 67 us are 5.3 TB/s, 80 % of the copy rate; H=3501 56 us. The copies alone take 40 us: what bounds
+// the pass is the latency of a warp's instructions (14 warps an SM, 45 % of issue slots used).
 template <int DT, int WT, int N, int K, bool kHold, bool kAligned>
 __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormBwdArgs a, int G, int R,
                                                             int S, int C) {
@@ -1141,36 +1058,43 @@ bool vector_rows(int vec, int64_t H, std::initializer_list<int64_t> strides,
 
 int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
 
+// Rows in registers: 16-byte accesses (VW elements), or single elements (VW = 1), which is for few
+// rows and for those that the staged form does not take (shorter than two windows or too wide).
 template <int DT, int WT, int VW>
 cudaError_t norm_forward_rows(const NormArgs& a, cudaStream_t s, bool* done) {
   const int64_t n = a.H / VW;  // accesses of a row (VW divides H)
-  constexpr int M = VW == 1 ? 16 : 4;  // of a thread, with many rows
   *done = true;
   const bool few = a.T < 2 * device_sm_count();
-  if (!few && n <= 64 * M) {
-    // A warp per row or two: no barrier.
-    auto k = n <= 32       ? norm_row_kernel<DT, WT, VW, 1, 2, true>
-             : n <= 64     ? norm_row_kernel<DT, WT, VW, 2, 2, true>
-             : n <= 32 * M ? norm_row_kernel<DT, WT, VW, M, 2, true>
-                           : norm_row_kernel<DT, WT, VW, 2 * M, 1, true>;
-    const int rows = kNormWarpRows * (n <= 32 * M ? 2 : 1);
-    return launch_pdl(k, dim3(static_cast<unsigned>((a.T + rows - 1) / rows)),
+  // A warp per row or two: no barrier.
+  auto warps = [&](auto kernel, int rows) {
+    rows *= kNormWarpRows;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>((a.T + rows - 1) / rows)),
                       dim3(32 * kNormWarpRows), 0, s, a);
+  };
+  if (!few && n <= 32) return warps(norm_row_kernel<DT, WT, VW, 1, 2, true>, 2);
+  if constexpr (VW > 1) {
+    if (!few && n <= 64) return warps(norm_row_kernel<DT, WT, VW, 2, 2, true>, 2);
+    if (!few && n <= 128) return warps(norm_row_kernel<DT, WT, VW, 4, 2, true>, 2);
+    if (!few && n <= 256) return warps(norm_row_kernel<DT, WT, VW, 8, 1, true>, 1);
   }
-  // A CTA per two rows; with few rows one each, and as many threads as the row has work for.
+  // A CTA per row; with few rows as many threads as the row has work for, with many two rows each
+  // (T=8192, H=7168 bf16: 45 us, a row each 56 us).
+  constexpr int M = VW == 1 ? 16 : 4;
   const int per = few && n <= 1024 ? 1 : few && n <= 2048 ? 2 : M;
   const int G = round32((n + per - 1) / per);
-  if (G <= 1024) {
-    const bool two = per == M && !few && G <= 512;
-    auto k = per == 1   ? norm_row_kernel<DT, WT, VW, 1, 1, false>
-             : per == 2 ? norm_row_kernel<DT, WT, VW, 2, 1, false>
-             : two      ? norm_row_kernel<DT, WT, VW, M, 2, false>
-                        : norm_row_kernel<DT, WT, VW, M, 1, false>;
-    const int64_t grid = two ? (a.T + 1) / 2 : a.T;
-    return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(G), 0, s, a);
+  if (G > 1024) {
+    *done = false;
+    return cudaSuccess;
   }
-  *done = false;
-  return cudaSuccess;
+  if constexpr (VW > 1) {
+    if (!few && G <= 512)
+      return launch_pdl(norm_row_kernel<DT, WT, VW, M, 2, false>,
+                        dim3(static_cast<unsigned>((a.T + 1) / 2)), dim3(G), 0, s, a);
+  }
+  auto k = per == 1   ? norm_row_kernel<DT, WT, VW, 1, 1, false>
+           : per == 2 ? norm_row_kernel<DT, WT, VW, 2, 1, false>
+                      : norm_row_kernel<DT, WT, VW, M, 1, false>;
+  return launch_pdl(k, dim3(static_cast<unsigned>(a.T)), dim3(G), 0, s, a);
 }
 
 // CTAs of a backward kernel: one an SM (a device-independent bound keeps the workspace the same).
@@ -1242,24 +1166,8 @@ int norm_forward(const NormArgs& a, cudaStream_t s) {
   return e == cudaSuccess ? 0 : MHC_ERR_CUDA;
 }
 
-// Launches the element-wise form and returns its number of partial rows, or 0 (nothing launched)
-// where the row is too wide for it.
-template <int DT, int WT>
-int norm_backward_rows(const NormBwdArgs& a, cudaStream_t s, cudaError_t* e) {
-  const int per = a.H <= 4096 ? 8 : 16;
-  const int G = round32((a.H + per - 1) / per);
-  if (G > 512) return 0;
-  const int R = G == 32 ? 16 : 512 / G < 15 ? 512 / G : 15;
-  const size_t smem = R > 1 ? static_cast<size_t>(R) * 2 * a.H * 4 : 0;
-  auto k = per == 8 ? norm_bwd_row_kernel<DT, WT, 8> : norm_bwd_row_kernel<DT, WT, 16>;
-  if (!ensure_smem_limit(reinterpret_cast<const void*>(k), static_cast<int>(smem))) return 0;
-  const unsigned grid = norm_bwd_grid((a.T + R - 1) / R);
-  *e = launch_pdl(k, dim3(grid), dim3(G * R), smem, s, a, G);
-  note_launches(1);
-  return static_cast<int>(grid);
-}
-
-// The staged form, likewise: rows that fit twice beside gamma.
+// Launches the staged form and returns its number of partial rows, or 0 (nothing launched) where two
+// stages of rows do not fit beside the weights (or rows are shorter than two windows).
 template <int DT, int WT, bool kAligned>
 int norm_backward_ring(const NormBwdArgs& a, cudaStream_t s, cudaError_t* e) {
   constexpr int VE = Elem<DT>::kVec, N = 16 / VE;  // windows of a thread that holds 16 columns
@@ -1290,7 +1198,6 @@ int norm_backward(NormBwdArgs a, float* dgamma, float* dbeta, cudaStream_t s) {
     rows = norm_backward_ring<DT, WT, true>(a, s, &e);
   else
     rows = norm_backward_ring<DT, WT, false>(a, s, &e);
-  if (rows == 0) rows = norm_backward_rows<DT, WT>(a, s, &e);
   if (rows == 0) {
     e = launch_pdl(norm_bwd_dx_loop_kernel<DT, WT>, dim3(row_grid(a.T)), dim3(kNormThreads), 0, s,
                    a);
