@@ -379,7 +379,11 @@ MHC_API int mhc_head(const uint16_t* R, const float* hc_fn, const float* hc_scal
  * The answer end of the stack: what follows a pre-map's y or a head's row, for training and serving.
  * No entry of these is on the pages; they are additions of this library. Rows lie `stride` elements
  * apart (stride >= the row's length, so a slice of wider rows or a padded vocabulary is taken as it
- * is), at any alignment of the element. Three element types:
+ * is), at any alignment of the element. Rows are read in whole 16-byte windows: beside a row's ends
+ * bytes of the same array (of the rows before and after, or the gap between) may be read along, never
+ * bytes before its first row or behind its last, and none is used or written. The same call on the
+ * same addresses gives the same bits; sums are grouped by windows, so another alignment of the output
+ * or another number of rows may round differently. Three element types:
  */
 enum mhc_dtype {
     MHC_DTYPE_BF16 = 0,
