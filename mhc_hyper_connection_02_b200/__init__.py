@@ -555,9 +555,9 @@ def _rows(t, name, shape=None, dtype=None, device=None):
 
 
 class _OtherStream:
-    """A call on a given stream (a torch stream or a handle). While it is entered, allocations
-    belong to that stream; at the end the tensors of the call are marked as used there, so that
-    memory freed on their own stream is not handed out again too early."""
+    """A call on a given stream (a torch stream or a handle). From enter on, allocations belong to
+    that stream; at the end the tensors of the call are marked as used there, so that memory freed
+    on their own stream is not handed out again too early."""
 
     def __init__(self, stream, device, tensors):
         import torch
@@ -572,39 +572,29 @@ class _OtherStream:
         self._tensors = tensors
         self._scope = torch.cuda.stream(stream) if self._other is not None else None
 
-    def __enter__(self):
+    def enter(self):
         if self._scope is not None:
             self._scope.__enter__()
         return self.handle
 
-    def __exit__(self, *exc):
+    def leave(self):
         if self._scope is not None:
             for t in self._tensors:
                 if t is not None:
                     t.record_stream(self._other)
-            self._scope.__exit__(*exc)
-        return False
+            self._scope.__exit__(None, None, None)
 
 
-class _CurrentStream:
-    """A call on the device's current stream."""
-
-    def __init__(self, device):
-        import torch
-        self.handle = torch._C._cuda_getCurrentRawStream(device.index)
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *exc):
-        return False
+def _current(device):
+    """Handle of the device's current stream."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _launch(stream, device, *tensors):
-    """The stream of a call on `device`: the given one, else the device's current one."""
-    if stream is None:
-        return _CurrentStream(device)
-    return _OtherStream(stream, device, tensors)
+def _dense_like(x):
+    """An uninitialised dense tensor of x's shape and type."""
+    import torch
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def _need_on(t, dtype, shape, name, device):
@@ -649,9 +639,12 @@ def layer_norm(x, gamma=None, beta=None, *, eps: float = 1e-6, y=None, mean=None
         _need_on(mean, torch.float32, (T,), "mean", dev)
     if rstd is not None:
         _need_on(rstd, torch.float32, (T,), "rstd", dev)
-    with _launch(stream, dev, x, gamma, beta, y, mean, rstd) as handle:
+    on = None if stream is None else _OtherStream(
+        stream, dev, (x, gamma, beta, y, mean, rstd))
+    handle = _current(dev) if on is None else on.enter()
+    try:
         if y is None:
-            y = x.new_empty((T, H))
+            y = _dense_like(x)
         if mean is None:
             mean = x.new_empty(T, dtype=torch.float32)
         if rstd is None:
@@ -659,6 +652,9 @@ def layer_norm(x, gamma=None, beta=None, *, eps: float = 1e-6, y=None, mean=None
         st = lib().mhc_layer_norm(_ptr(x), stride, _codes[x.dtype], _ptr(gamma), _ptr(beta),
                                   wd if wd is not None else bd if bd is not None else DTYPE_F32,
                                   _ptr(y), _ptr(mean), _ptr(rstd), T, H, float(eps), handle)
+    finally:
+        if on is not None:
+            on.leave()
     _check(st, "mhc_layer_norm")
     return y, mean, rstd
 
@@ -682,9 +678,12 @@ def layer_norm_backward(d_y, x, gamma, mean, rstd, *, d_x=None, workspace=None, 
         _need_on(d_x, x.dtype, (T, H), "d_x", dev)
     if workspace is not None:
         _need_on(workspace, workspace.dtype, None, "workspace", dev)
-    with _launch(stream, dev, d_y, x, gamma, mean, rstd, d_x, workspace) as handle:
+    on = None if stream is None else _OtherStream(
+        stream, dev, (d_y, x, gamma, mean, rstd, d_x, workspace))
+    handle = _current(dev) if on is None else on.enter()
+    try:
         if d_x is None:
-            d_x = x.new_empty((T, H))
+            d_x = _dense_like(x)
         d_gamma = mean.new_empty(H)
         d_beta = mean.new_empty(H)
         if workspace is None and T > 0:
@@ -694,6 +693,9 @@ def layer_norm_backward(d_y, x, gamma, mean, rstd, *, d_x=None, workspace=None, 
             _ptr(d_y), ds, _ptr(x), xs, _codes[x.dtype], _ptr(gamma),
             DTYPE_F32 if wd is None else wd, _ptr(mean), _ptr(rstd), _ptr(d_x), _ptr(d_gamma),
             _ptr(d_beta), _ptr(workspace), wsb, T, H, handle)
+    finally:
+        if on is not None:
+            on.leave()
     _check(st, "mhc_layer_norm_backward")
     return d_x, d_gamma, d_beta
 
@@ -704,7 +706,7 @@ def _grad_rows(logits, T, V, stride):
     next product wants its rows aligned as well."""
     if V < stride <= V + V // 8:
         return logits.new_empty((T, stride))[:, :V]
-    return logits.new_empty((T, V))
+    return _dense_like(logits)
 
 
 def token_logprobs(logits, targets=None, *, temperature: float = 1.0, top: int = 0,
@@ -722,7 +724,9 @@ def token_logprobs(logits, targets=None, *, temperature: float = 1.0, top: int =
         raise ValueError(f"top must be 0 to min(V, {TOP_MAX})")
     if targets is not None:
         _need_on(targets, torch.int64, (T,), "targets", dev)
-    with _launch(stream, dev, logits, targets) as handle:
+    on = None if stream is None else _OtherStream(stream, dev, (logits, targets))
+    handle = _current(dev) if on is None else on.enter()
+    try:
         stats = logits.new_empty((T, 2), dtype=torch.float32)
         lp = stats.new_empty(T) if targets is not None else None
         ent = stats.new_empty(T) if entropy else None
@@ -731,6 +735,9 @@ def token_logprobs(logits, targets=None, *, temperature: float = 1.0, top: int =
         st = lib().mhc_token_logprobs(_ptr(logits), stride, _codes[logits.dtype], _ptr(targets),
                                       float(temperature), _ptr(lp), _ptr(ent), top, _ptr(ti),
                                       _ptr(tl), _ptr(stats), T, V, handle)
+    finally:
+        if on is not None:
+            on.leave()
     _check(st, "mhc_token_logprobs")
     return lp, ent, ti, tl, stats
 
@@ -752,8 +759,10 @@ def token_logprobs_backward(logits, targets, stats, d_logprob=None, *, d_entropy
     for name, t in (("d_logprob", d_logprob), ("d_entropy", d_entropy), ("entropy", entropy)):
         if t is not None:
             _need_on(t, torch.float32, (T,), name, dev)
-    with _launch(stream, dev, logits, targets, stats, d_logprob, d_entropy, entropy,
-                 d_logits) as handle:
+    on = None if stream is None else _OtherStream(
+        stream, dev, (logits, targets, stats, d_logprob, d_entropy, entropy, d_logits))
+    handle = _current(dev) if on is None else on.enter()
+    try:
         if d_logits is None:
             d_logits = _grad_rows(logits, T, V, stride)
         ds = _rows(d_logits, "d_logits", (T, V), logits.dtype, dev)
@@ -761,6 +770,9 @@ def token_logprobs_backward(logits, targets, stats, d_logprob=None, *, d_entropy
             _ptr(logits), stride, _codes[logits.dtype], _ptr(targets), float(temperature),
             _ptr(stats), _ptr(d_logprob), _ptr(d_entropy), _ptr(entropy), _ptr(d_logits), ds, T, V,
             handle)
+    finally:
+        if on is not None:
+            on.leave()
     _check(st, "mhc_token_logprobs_backward")
     return d_logits
 
@@ -785,13 +797,18 @@ def distill_topk(logits, index, teacher, *, temperature: float = 1.0, stream=Non
     K = _entries(index, T, dev)
     td = _dtype(teacher, "teacher")
     _need_on(teacher, teacher.dtype, (T, K), "teacher", dev)
-    with _launch(stream, dev, logits, index, teacher) as handle:
+    on = None if stream is None else _OtherStream(stream, dev, (logits, index, teacher))
+    handle = _current(dev) if on is None else on.enter()
+    try:
         stats = logits.new_empty((T, 2), dtype=torch.float32)
         loss = stats.new_empty(T)
         weights = stats.new_empty((T, K))
         st = lib().mhc_distill_topk(_ptr(logits), stride, _codes[logits.dtype], _ptr(index),
                                     _ptr(teacher), td, float(temperature), _ptr(loss),
                                     _ptr(weights), _ptr(stats), T, V, K, handle)
+    finally:
+        if on is not None:
+            on.leave()
     _check(st, "mhc_distill_topk")
     return loss, weights, stats
 
@@ -809,13 +826,19 @@ def distill_topk_backward(logits, index, weights, stats, d_loss, *, temperature:
     _need_on(weights, torch.float32, (T, K), "weights", dev)
     _need_on(stats, torch.float32, (T, 2), "stats", dev)
     _need_on(d_loss, torch.float32, (T,), "d_loss", dev)
-    with _launch(stream, dev, logits, index, weights, stats, d_loss, d_logits) as handle:
+    on = None if stream is None else _OtherStream(
+        stream, dev, (logits, index, weights, stats, d_loss, d_logits))
+    handle = _current(dev) if on is None else on.enter()
+    try:
         if d_logits is None:
             d_logits = _grad_rows(logits, T, V, stride)
         ds = _rows(d_logits, "d_logits", (T, V), logits.dtype, dev)
         st = lib().mhc_distill_topk_backward(
             _ptr(logits), stride, _codes[logits.dtype], _ptr(index), _ptr(weights), _ptr(stats),
             _ptr(d_loss), float(temperature), _ptr(d_logits), ds, T, V, K, handle)
+    finally:
+        if on is not None:
+            on.leave()
     _check(st, "mhc_distill_topk_backward")
     return d_logits
 
