@@ -10,8 +10,8 @@
 // The variance is formed from the differences to the mean (a second walk over the row), not from
 // sum(x^2) - mean^2, which loses every digit where |mean| is large against the deviation. All sums
 // and statistics are fp32; y and d_x are rounded once. Sums over tokens are in a fixed order: each
-// CTA adds its tokens in order into a partial row of the workspace, and a second kernel adds the
-// partial rows in order.
+// group of a CTA adds its tokens in order, the CTA its groups into a partial row of the workspace, and
+// a second kernel adds the partial rows in order.
 #include <math.h>
 
 #include <initializer_list>
