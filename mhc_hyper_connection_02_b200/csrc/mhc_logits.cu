@@ -83,6 +83,12 @@ __device__ __forceinline__ RowPart row_part(const void* row, int n, int rank, in
   return p;
 }
 
+// Where a thread's maximum was met first, and the largest maximum of its other rounds.
+struct ThreadBest {
+  int round;     // first window of that round of kLgUnroll
+  float second;
+};
+
 // This thread's sums over its windows of the part: first + tid, + NT, .... The usual d is one fma,
 // z c - mc with mc = m c rounded: every d is off by mc's rounding, which the end takes out again.
 // Where mc overflows (the lowest finite values, or an infinity) d is (z - m) c.
@@ -92,11 +98,6 @@ __device__ __forceinline__ RowPart row_part(const void* row, int n, int rank, in
 // T=8192, V=131072, bf16: 303 us, with entropy 314 us (7.1 and 6.8 TB/s) in a burst, without packed
 // values and pairs 352 and 406 us; under seconds of load the SMs' clock falls to 1.56 GHz at the power
 // cap, and ex2 brings them to 357 and 383 us.
-// best: where this thread's maximum was met first, and the largest maximum of its other rounds.
-struct ThreadBest {
-  int round;     // first window of that round of kLgUnroll
-  float second;
-};
 template <int DT, int NT, bool kEnt>
 __device__ __forceinline__ RowSums thread_sums(const typename Elem<DT>::raw* row, const RowPart& p,
                                                float c, ThreadBest& best) {
