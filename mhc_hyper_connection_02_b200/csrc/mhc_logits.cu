@@ -93,8 +93,8 @@ struct ThreadBest {
 // z c - mc with mc = m c rounded: every d is off by mc's rounding, which the end takes out again.
 // Where mc overflows (the lowest finite values, or an infinity) d is (z - m) c.
 //
-// ex2 runs at 16 a clock and SM, which leaves 8 of the 11 issue slots that HBM's rate allows an
-// element of bf16: the rest is therefore done on packed values (maximum, cut) and on pairs of fp32.
+// ex2 runs at 16 a clock and SM: a warp's takes 8 of the 11 cycles that HBM's rate allows an element
+// of bf16. The rest is therefore done on packed values (maximum, cut) and on pairs of fp32.
 // T=8192, V=131072, bf16: 303 us, with entropy 314 us (7.1 and 6.8 TB/s) in a burst, without packed
 // values and pairs 352 and 406 us; under seconds of load the SMs' clock falls to 1.56 GHz at the power
 // cap, and ex2 brings them to 357 and 383 us.
