@@ -159,6 +159,12 @@ __device__ __forceinline__ void bulk_g2s(void* smem_dst, const void* gmem_src, u
       : "memory");
 }
 
+// Orders this thread's plain accesses to shared memory before later ones of the async proxy (bulk
+// copies, MMA operands).
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // Named barrier over `nthreads` threads that also ORs a predicate: every participant gets the same
 // answer, so a decision taken on it (such as stopping after a timeout) keeps the barrier sequence
 // matched.

@@ -364,9 +364,11 @@ struct RowRing {
   __device__ __forceinline__ int windows(int i) const {
     return kAligned ? H / VE : (off[i] + H + VE - 1) / VE;
   }
-  // The same with rows that an array begins or ends with: only the windows that such a row fills.
+  // The same with rows that an array begins or ends with: only the windows that such a row fills,
+  // and its other elements one by one. Those are stored before the arrival, which releases them to
+  // whoever waits on the stage, and the fence puts them before copies that overwrite them later.
   __device__ __noinline__ void copy_ends(int st, uint32_t j) const {
-    for (int turn = 0; turn < 2; ++turn) {  // the sum of bytes, then the copies
+    for (int turn = 0; turn < 2; ++turn) {  // elements and the sum of bytes, then the copies
       uint32_t bytes = 0;
       for (int r = 0; r < K; ++r)
         for (int i = 0; i < A; ++i) {
@@ -375,16 +377,21 @@ struct RowRing {
           const int64_t t = token(at);
           const int from = t == 0 && off[i] > 0 ? 1 : 0;
           const int to = t == tokens - 1 ? (off[i] + H) / VE : windows(i);
-          bytes += (to - from) * 16;
-          if (turn == 0) continue;
           uint4* slot_of = slot_at(st, r, i) + 1;
-          raw* elements = reinterpret_cast<raw*>(slot_of) + off[i];
-          if (from > 0)
-            for (int e = 0; e < VE - off[i]; ++e) elements[e] = row[e];
-          for (int e = to * VE - off[i]; e < H; ++e) elements[e] = row[e];
-          bulk_g2s(slot_of + from, row - off[i] + from * VE, (to - from) * 16, &full[st]);
+          if (turn == 0) {
+            bytes += (to - from) * 16;
+            raw* elements = reinterpret_cast<raw*>(slot_of) + off[i];
+            if (from > 0)
+              for (int e = 0; e < VE - off[i]; ++e) elements[e] = row[e];
+            for (int e = to * VE - off[i]; e < H; ++e) elements[e] = row[e];
+          } else {
+            bulk_g2s(slot_of + from, row - off[i] + from * VE, (to - from) * 16, &full[st]);
+          }
         }
-      if (turn == 0) mbar_arrive_expect_tx(&full[st], bytes);
+      if (turn == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(&full[st], bytes);
+      }
     }
   }
   // The first S stages.

@@ -140,10 +140,6 @@ __device__ __forceinline__ void pp_issue_block(int64_t g, int64_t hb, int s, uin
   cp_async_commit();
 }
 
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 __global__ void __launch_bounds__(kPpThreads, 1) post_project_kernel(
     const __grid_constant__ CUtensorMap tmB, const uint16_t* __restrict__ x, const uint16_t* R,
     const float* __restrict__ post, const float* __restrict__ comb, uint16_t* out,

@@ -254,3 +254,23 @@ def test_training_batch():
     n = -(-T // 64) + 100
     check(dg, f64(tot[0]), (n + 4) * 2.0 ** -24 * f64(tot[2]), "d_gamma")
     check(db, f64(tot[1]), n * 2.0 ** -24 * f64(tot[3]), "d_beta")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [1, 2, 9, 321, 2001])
+def test_the_first_and_the_last_row_of_an_array(dtype, T):
+    """Rows of one value set give one result wherever they stand: the first and the last row, whose
+    ends are fetched element by element, and those between them (of one phase, so of one grouping of
+    the sums). Fresh values each time: what an earlier call left in shared memory shows."""
+    for i, H in enumerate((1001, 77, 3501, 9003) * 6):
+        x1, dy1, gamma, beta = _make(8, H, dtype, "fp32", i)
+        at = torch.arange(T, device="cuda") % 8
+        nan = float("nan")
+        x, bx = _rows_at(x1[at], 3, H, nan)
+        dy, bd = _rows_at(dy1[at], 1, H, nan)
+        y, mean, rstd = mhc.layer_norm(x, gamma, beta)
+        dx = mhc.layer_norm_backward(dy, x, gamma, mean, rstd)[0]
+        for a in (y, dx):
+            assert torch.equal(a, a[at]), (H, i)
+        if i < 4:
+            _check_forward(x1[at[-1:]], gamma, beta, (y[-1:], mean[-1:], rstd[-1:]), dtype)
