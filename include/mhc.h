@@ -443,8 +443,8 @@ enum {
  *
  * mhc_token_logprobs_backward  d_logits = (d_logprob (1[v = target] - p_v)
  *                                          - d_entropy p_v (ln p_v + entropy)) / temperature
- *   d_logprob, d_entropy [T] fp32, one of them may be NULL (zero); entropy as the forward pass gave
- *   it (with d_entropy); targets with d_logprob. d_logits [T][V] of dtype, rows d_row_stride apart,
+ *   d_logprob, d_entropy [T] fp32, one of them may be NULL (zero), finite in fp32 when divided by
+ *   temperature; entropy as the forward pass gave it (with d_entropy); targets with d_logprob. d_logits [T][V] of dtype, rows d_row_stride apart,
  *   rounded once; may be exactly logits (same stride). Rows whose upstream gradients are zero get
  *   zeros, whatever their logits. The top alternatives have no gradient.
  * temperature: finite and > 0 (and so are 1 / temperature and log2(e) / temperature).

@@ -681,13 +681,17 @@ __device__ __forceinline__ uint4 load_window_rw(const typename Elem<DT>::raw* ro
 // The constants of a row's gradient: e (fb d + fa) with e = 2^d (kEnt; e fa otherwise).
 struct GradRow {
   float c, m, mc, fa, fb;
-  bool usual;  // d by one fma
+  bool usual;  // d by one fma, and the bracket is formed before the product with e
 };
 template <int DT, bool kEnt>
 __device__ __forceinline__ GradRow grad_row(float c, float m, float A, float B) {
   GradRow g;
   g.c = c, g.m = m, g.mc = __fmul_rn(m, c);
   g.usual = small_mc(g.mc) && (!kEnt || cut_ok<DT>(c));
+  // A masked logit's e is 0: in the usual form its bracket has to stay finite at the lowest d that
+  // the cuts leave, or the product would be NaN.
+  if constexpr (kEnt)
+    g.usual = g.usual && fmaf(fabsf(B), Elem<DT>::kCuts ? c * 0x1p100f : -kDCut, fabsf(A)) < 1e38f;
   // What every d of the usual form is too large by (see thread_sums): taken out of the constants.
   const float off = g.usual ? fmaf(m, c, -g.mc) : 0.0f;
   g.fa = ex2(-off) * fmaf(-B, off, A);
@@ -708,8 +712,10 @@ __device__ __forceinline__ void grad_window(uint4 w, const GradRow& g, float (&x
     else
       d = f2((x[q] - g.m) * g.c, (x[q + 1] - g.m) * g.c);
     F2 e = ex2(d);
-    if constexpr (kEnt)
-      e = e * fma2(f2(g.fb), E::kCuts && kUsual ? d : max2(d, kDCut), f2(g.fa));
+    if constexpr (kEnt && kUsual)
+      e = e * fma2(f2(g.fb), E::kCuts ? d : max2(d, kDCut), f2(g.fa));
+    else if constexpr (kEnt)
+      e = fma2(e * max2(d, kDCut), f2(g.fb), e * f2(g.fa));
     else
       e = e * f2(g.fa);
     const float2 v = split(e);

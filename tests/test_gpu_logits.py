@@ -508,3 +508,29 @@ def test_the_answer_end_of_a_stack():
     check(dx, dxo, lim, "d_x")
     check(dg, dgo, T * lim * 8, "d_gamma")
     check(db, dbo, T * lim * 8, "d_beta")
+
+
+@pytest.mark.parametrize("dtype,tau,size", [("bf16", 1e-3, 1e6), ("bf16", 1e-4, 1e4),
+                                            ("bf16", 1.0, 1e12), ("bf16", 1e-2, 1e35),
+                                            ("fp32", 1e-2, 1e35), ("fp16", 1e-3, 1e-3)])
+def test_entropy_gradient_of_masked_logits_under_a_large_scale(dtype, tau, size):
+    """A masked logit's gradient is zero, however large d_entropy / temperature is. The others lie
+    within 40 temperatures of the best, so that no probability is below the smallest normal
+    number."""
+    T, V = 6, 5003
+    g = torch.Generator().manual_seed(T)
+    z = (tau * 40 * torch.rand((T, V), generator=g)).to(DTYPES[dtype])
+    z[:, ::3] = -float("inf")
+    z[1, ::2] = torch.finfo(DTYPES[dtype]).min
+    z[2, 1:] = -float("inf")
+    z[2, 0] = tau
+    z[3] = -float("inf")
+    z[4, 7] = -float("inf")
+    z, y = z.cuda(), _targets(T, V, 1)
+    y[4] = 7                                        # the target itself is ruled out
+    _, ent, _, _, st = mhc.token_logprobs(z, y, temperature=tau)
+    a, b = size * torch.randn(T, device="cuda"), size * torch.randn(T, device="cuda")
+    for glp in (None, a):
+        d = mhc.token_logprobs_backward(z, y, st, glp, d_entropy=b, entropy=ent, temperature=tau)
+        _check_backward(z, y, tau, glp, b, st, ent, d, dtype)
+        assert not d[3].any() and not d[0, 3::3][: V // 8].isnan().any()
