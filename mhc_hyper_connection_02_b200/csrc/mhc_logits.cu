@@ -62,6 +62,19 @@ __device__ __forceinline__ float shift_of(float from, float to, float c) {
   return from == -INFINITY ? -1000.0f : fmaxf((from - to) * c, -1000.0f);  // -inf: nothing summed
 }
 
+// The same for a thread's running sums, which stand on what their d was formed with: the rounded mc
+// where that is small, else m c itself. A change from one to the other takes mc's rounding, up to a
+// quarter, out again or in.
+__device__ __forceinline__ float shift_between(float from, float mc_from, float to, float mc_to,
+                                               float c) {
+  if (from == -INFINITY) return -1000.0f;
+  if (small_mc(mc_from) && small_mc(mc_to)) return fmaxf(mc_from - mc_to, -1000.0f);
+  float d = (from - to) * c;
+  if (small_mc(mc_from)) d -= fmaf(from, c, -mc_from);
+  if (small_mc(mc_to)) d += fmaf(to, c, -mc_to);
+  return fmaxf(d, -1000.0f);
+}
+
 struct RowSums {
   float m, s, u;
 };
@@ -122,8 +135,7 @@ __device__ __forceinline__ RowSums thread_sums(const typename Elem<DT>::raw* row
     if (tm > r.m) {
       best.round = s0;
       const float mcn = __fmul_rn(tm, c);
-      float d = shift_of(r.m, tm, c);
-      if (r.m != -INFINITY && small_mc(mc) && small_mc(mcn)) d = fmaxf(mc - mcn, -1000.0f);
+      const float d = shift_between(r.m, mc, tm, mcn, c);
       const F2 f = f2(ex2(d));
       if constexpr (kEnt) u2 = f * fma2(f2(d), s2, u2);
       s2 = f * s2;

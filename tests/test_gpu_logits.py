@@ -534,3 +534,32 @@ def test_entropy_gradient_of_masked_logits_under_a_large_scale(dtype, tau, size)
         d = mhc.token_logprobs_backward(z, y, st, glp, d_entropy=b, entropy=ent, temperature=tau)
         _check_backward(z, y, tau, glp, b, st, ent, d, dtype)
         assert not d[3].any() and not d[0, 3::3][: V // 8].isnan().any()
+
+
+@pytest.mark.parametrize("tau", [1.0, 1e-3, 1e-6])
+@pytest.mark.parametrize("V,reps", [(9000, 30), (140001, 1)])
+def test_maxima_on_either_side_of_the_forms_border(tau, V, reps):
+    """The exponents' form changes where |max z| log2(e) / temperature passes 2^22. A thread's
+    maximum passes it from round to round of its windows (4096 elements), from below, from above
+    (negative logits) and not at all; the logits lie within 20 temperatures of one another."""
+    border = 2.0 ** 22 * LN2 * tau
+    steps = [(-9, -2, 4), (-3, 5, 6), (-12, -11, 1), (1, 3, 7), (-8, -6, -4), (6, -5, 9)]
+    g = torch.Generator().manual_seed(V)
+    at = torch.arange(V) // 4096 % 3
+    z = torch.stack([s * border + tau * (torch.tensor(p, dtype=torch.float64)[at]
+                                         + 2 * torch.rand(V, generator=g, dtype=torch.float64))
+                     for s in (1, -1) for p in steps]).float().cuda()
+    T = z.shape[0]
+    y = _targets(T, V, 1)
+    zz, yy = z.repeat(reps, 1), y.repeat(reps)
+    got = [None if v is None else v[-T:] for v in
+           mhc.token_logprobs(zz, yy, temperature=tau, top=4)]
+    _check_forward(z, y, tau, 4, got)
+    plain = mhc.token_logprobs(zz, yy, temperature=tau, entropy=False)
+    _check_forward(z, y, tau, 0, [plain[0][-T:], None, None, None, plain[4][-T:]])
+    a, b = torch.randn(T, device="cuda"), torch.randn(T, device="cuda")
+    d = mhc.token_logprobs_backward(z, y, got[4], a, d_entropy=b, entropy=got[1], temperature=tau)
+    _check_backward(z, y, tau, a, b, got[4], got[1], d, "fp32")
+    idx, t = _teacher(T, V, 5, "fp32", 2)
+    k = mhc.distill_topk(z, idx, tau * t, temperature=tau)
+    _check_distill(z, idx, tau * t, tau, k, "fp32")
