@@ -563,8 +563,13 @@ class _OtherStream:
         import torch
         current = torch.cuda.current_stream(device)
         if not isinstance(stream, torch.cuda.Stream):
-            stream = current if int(stream) == current.cuda_stream else \
-                torch.cuda.ExternalStream(int(stream), device=device)
+            handle = int(getattr(stream, "cuda_stream", stream))
+            if handle == current.cuda_stream:
+                stream = current
+            elif handle == 0:  # which ExternalStream would take for "any stream"
+                stream = torch.cuda.default_stream(device)
+            else:
+                stream = torch.cuda.ExternalStream(handle, device=device)
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
         self.handle = int(stream.cuda_stream)

@@ -274,3 +274,20 @@ def test_the_first_and_the_last_row_of_an_array(dtype, T):
             assert torch.equal(a, a[at]), (H, i)
         if i < 4:
             _check_forward(x1[at[-1:]], gamma, beta, (y[-1:], mean[-1:], rstd[-1:]), dtype)
+
+
+def test_the_default_stream_by_its_handle():
+    """Handle 0 is the device's default stream, whichever stream is current: the call comes after
+    what stands in that stream."""
+    x, dy, gamma, beta = _make(64, 1000, "bf16", "fp32", 3)
+    ref = mhc.layer_norm(x, gamma, beta)
+    late, out = torch.zeros_like(x), [torch.empty_like(v) for v in ref]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # clocks: some 50 ms
+    late.copy_(x)
+    with torch.cuda.stream(side):
+        mhc.layer_norm(late, gamma, beta, y=out[0], mean=out[1], rstd=out[2], stream=0)
+    torch.cuda.synchronize()
+    for g, w in zip(out, ref):
+        assert torch.equal(g, w)
