@@ -830,17 +830,15 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
     if (G == 32) __syncwarp();
     if (tid == 0 && (kHold || lap + st > 0) && next < rr.T)
       plan().copy(kHold ? st : st > 0 ? st - 1 : S - 1, next);
-    // d_x = r d_y gamma - r c1 - (x - mean) r^2 c2 = r (d_y gamma) + (x' f + f0). For 16-bit rows x' is
-    // x and the mean's part in f0: off by 2^-24 |mean| r of the last term, where a row of such a type
-    // has |mean| r below its own 2^8 or 2^11 steps. fp32 rows take x' = x - mean.
-    constexpr bool kFold = DT != 2;
+    // d_x = r d_y gamma - r c1 - (x - mean) r^2 c2 = r (d_y gamma) + ((x - mean) f + f0). x - mean is
+    // formed first for every type: taken into f0 the mean's part would be off by 2^-24 |mean| r of
+    // the last term, and a 16-bit row can have |mean| r above 10^4 (few values a step from the rest).
     F2 f0[K], fx[K];
 #pragma unroll
     for (int r = 0; r < K; ++r) {
       const float f = -rs[r] * rs[r] * (rs[r] * sums[2 * r + 1] * per_h);
       fx[r] = f2(f);
-      const float c = -rs[r] * (sums[2 * r] * per_h);
-      f0[r] = f2(kFold ? fmaf(split(nm[r]).x, f, c) : c);
+      f0[r] = f2(-rs[r] * (sums[2 * r] * per_h));
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -856,7 +854,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormB
           unpack_pairs<DT>(kHold ? hd[r][i] : rr.window(st, r, 1, at), d);
 #pragma unroll
           for (int q = 0; q < P; ++q)
-            x[q] = fma2(d[q] * g[q], fr[r], fma2(kFold ? x[q] : x[q] + nm[r], fx[r], f0[r]));
+            x[q] = fma2(d[q] * g[q], fr[r], fma2(x[q] + nm[r], fx[r], f0[r]));
           put_window<DT, kAligned>(dx + static_cast<int64_t>(r) * rr.classes * a.H, a.H,
                                    at * VE - off, x);
         }

@@ -291,3 +291,24 @@ def test_the_default_stream_by_its_handle():
     torch.cuda.synchronize()
     for g, w in zip(out, ref):
         assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("dtype,low,high", [("fp16", 2000.0, 2001.0), ("bf16", 1000.0, 1004.0)])
+@pytest.mark.parametrize("H", [264, 1000, 1001, 7168, 9000, 9001])
+def test_gradient_of_rows_of_two_neighbouring_values(dtype, low, high, H):
+    """16-bit rows whose deviation is far below a step of their mean, with d_y along x - mean, so
+    that d_x is a small difference: x - mean has to be formed first (the bound of fp32 rows)."""
+    T = 300
+    g = torch.Generator().manual_seed(H)
+    x = torch.where(torch.rand((T, H), generator=g) < 0.01, high, low)
+    x[:, 5] = high
+    x = x.to(DTYPES[dtype]).cuda()
+    _, mean, rstd = mhc.layer_norm(x)
+    dy = ((x.float() - mean[:, None]) * rstd[:, None]).to(DTYPES[dtype])
+    got = mhc.layer_norm_backward(dy, x, None, mean, rstd)
+    a = [f64(dy), f64(x), None, f64(mean), f64(rstd)]
+    dx, dg, db = rows.layer_norm_backward(*a)
+    ex, eg, eb = norm_bwd_bounds(*a)
+    check(got[0], dx, rounded(dx, ex, dtype), "d_x")
+    check(got[1], dg, eg, "d_gamma")
+    check(got[2], db, eb, "d_beta")
