@@ -207,8 +207,10 @@ MHC_API int mhc_device_status(mhc_stream_t stream);
  * pages). Enqueues one kernel whose single thread waits on an mbarrier that nothing arrives at,
  * through the same wait routine every pipeline uses, but with limit_ns (1 us .. 1 s) instead of the
  * library-wide 2 s. The wait runs out, the kernel records MHC_ERR_TIMEOUT in the device status word
- * and returns; no copy is in flight, so the context stays usable. A following mhc_device_status()
- * returns MHC_ERR_TIMEOUT (and clears the word). Errors: MHC_ERR_INVALID_ARG (limit out of range),
+ * and returns; no copy is in flight, so the context stays usable. With the timeout recorded it also
+ * makes a wait of the kind that kernels end with (for their own copies in flight), which has to last
+ * until its arrival half a limit later. A following mhc_device_status() returns MHC_ERR_TIMEOUT
+ * (and clears the word), or MHC_ERR_CUDA where that second wait gave up. Errors: MHC_ERR_INVALID_ARG (limit out of range),
  * MHC_ERR_UNSUPPORTED (current device not sm_100), MHC_ERR_CUDA (launch failed). */
 MHC_API int mhc_selftest_wait_timeout(int64_t limit_ns, mhc_stream_t stream);
 

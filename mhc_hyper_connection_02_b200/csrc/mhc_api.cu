@@ -64,13 +64,25 @@ static std::atomic<uint64_t> g_launches{0};
 
 // Health check of the bounded waits: one thread waits on an mbarrier that nothing arrives at, with
 // the caller's limit instead of the library-wide one, through the same wait routine the pipelines
-// use. No copy or MMA is in flight, so giving up leaves nothing behind.
+// use. Then, with that timeout recorded, it waits as for a copy in flight, on an mbarrier at which a
+// thread of another warp arrives half the limit later: this wait must not give up. No copy or MMA
+// is in flight, so giving up leaves nothing behind.
 __global__ void selftest_wait_kernel(unsigned long long limit_ns) {
-  __shared__ uint64_t bar;
+  __shared__ uint64_t bar, late;
+  const unsigned long long t0 = global_timer_ns();
   if (threadIdx.x == 0) {
     mbar_init(&bar, 1);
+    mbar_init(&late, 1);
     fence_mbarrier_init();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
     mbar_wait_for(&bar, 0, 99, limit_ns);
+    if (!mbar_wait_for<true>(&late, 0, 99, limit_ns))
+      atomicExch(&g_device_status, static_cast<int>(MHC_ERR_CUDA));
+  } else if (threadIdx.x == 32) {
+    while (global_timer_ns() - t0 < limit_ns + limit_ns / 2) __nanosleep(1000);
+    mbar_arrive(&late);
   }
 }
 void note_launches(int n) { g_launches.fetch_add(static_cast<uint64_t>(n), std::memory_order_relaxed); }
@@ -568,7 +580,7 @@ int mhc_selftest_wait_timeout(int64_t limit_ns, mhc_stream_t stream) {
   const int dev = current_device();
   if (dev < 0) return MHC_ERR_CUDA;
   if (device_cc() / 10 != 10) return MHC_ERR_UNSUPPORTED;
-  selftest_wait_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+  selftest_wait_kernel<<<1, 64, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       static_cast<unsigned long long>(limit_ns));
   note_launches(1);
   return cudaGetLastError() == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;

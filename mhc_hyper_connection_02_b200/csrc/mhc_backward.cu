@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kPbThreads, kPbCtas) post_bwd_persistent_kerne
       if (!ok) {
         for (int i = 0; i < kPbStages; ++i) {
           const int64_t n_i = issued / kPbStages + (i < issued % kPbStages ? 1 : 0);
-          if (n_i > 0) mbar_wait(&full[i], static_cast<uint32_t>((n_i - 1) & 1), 122);
+          if (n_i > 0) mbar_drain(&full[i], static_cast<uint32_t>((n_i - 1) & 1), 122);
         }
       }
     }

@@ -370,12 +370,12 @@ __global__ void __launch_bounds__(kDrThreads, 1)
       if (!ok) {
         for (int64_t k = it - kDrRSlots; k < it; ++k)
           if (k >= 0)
-            mbar_wait(&rfull[k % kDrRSlots], static_cast<uint32_t>(k / kDrRSlots) & 1u, 93);
+            mbar_drain(&rfull[k % kDrRSlots], static_cast<uint32_t>(k / kDrRSlots) & 1u, 93);
         for (int64_t k = nbl - kDrBSlots; k < nbl; ++k)
           if (k >= 0)
-            mbar_wait(&bfull[k % kDrBSlots], static_cast<uint32_t>(k / kDrBSlots) & 1u, 93);
-        if (ng > 0) mbar_wait(&dyfull[(ng - 1) & 1], static_cast<uint32_t>((ng - 1) >> 1) & 1u, 93);
-        if (ng > 1) mbar_wait(&dyfull[(ng - 2) & 1], static_cast<uint32_t>((ng - 2) >> 1) & 1u, 93);
+            mbar_drain(&bfull[k % kDrBSlots], static_cast<uint32_t>(k / kDrBSlots) & 1u, 93);
+        if (ng > 0) mbar_drain(&dyfull[(ng - 1) & 1], static_cast<uint32_t>((ng - 1) >> 1) & 1u, 93);
+        if (ng > 1) mbar_drain(&dyfull[(ng - 2) & 1], static_cast<uint32_t>((ng - 2) >> 1) & 1u, 93);
       }
     }
   } else if (warp == 1) {
@@ -463,9 +463,9 @@ __global__ void __launch_bounds__(kDrThreads, 1)
         }
       }
       // Do not leave while an A load is in flight.
-      if (!ok && na_issued > na) mbar_wait(abar, static_cast<uint32_t>(na) & 1u, 93);
+      if (!ok && na_issued > na) mbar_drain(abar, static_cast<uint32_t>(na) & 1u, 93);
       umma_commit(done);  // every issued MMA has finished before TMEM is released
-      mbar_wait(done, 0, 98);
+      mbar_drain(done, 0, 98);
     }
   } else if (warp < 6) {
     // ------------------------------------------------------------------ epilogue
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kWtThreads, 2) pre_bwd_dw_kernel_tc(
       if (!ok) {  // do not leave while copies into shared memory are in flight
         for (int64_t i = n - kWtStages; i < n; ++i)
           if (i >= 0)
-            mbar_wait(&full[i % kWtStages], static_cast<uint32_t>(i / kWtStages) & 1u, 111);
+            mbar_drain(&full[i % kWtStages], static_cast<uint32_t>(i / kWtStages) & 1u, 111);
       }
     }
   } else if (warp == 1) {
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(kWtThreads, 2) pre_bwd_dw_kernel_tc(
         u += tbe - tbs;
       }
       umma_commit(done);
-      mbar_wait(done, 0, 114);
+      mbar_drain(done, 0, 114);
     }
   } else {
     // Warps 2..5: TMEM lane quarter q holds features 32q .. 32q + 31 of the tile.

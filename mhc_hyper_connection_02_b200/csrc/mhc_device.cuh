@@ -127,7 +127,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 // Wait for the phase with the given parity to complete. Returns false (and records a timeout) if
 // it has not completed within limit_ns; the caller then stops using the pipeline. Also returns
-// false once another wait has recorded a timeout.
+// false once another wait has recorded a timeout, except with kDrain.
+template <bool kDrain = false>
 __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, int where,
                                               unsigned long long limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -135,7 +136,7 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, in
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 255u) == 0) {
-      if (*reinterpret_cast<volatile int*>(&g_device_status) != 0) return false;
+      if (!kDrain && *reinterpret_cast<volatile int*>(&g_device_status) != 0) return false;
       if (global_timer_ns() - t0 > limit_ns) {
         report_timeout(where);
         return false;
@@ -146,6 +147,11 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, in
 // The kernels' waits use the library-wide limit.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int where) {
   return mbar_wait_for(bar, parity, where, kWaitLimitNs);
+}
+// Before a CTA gives up its shared memory or TMEM: waits for its own copies or MMAs in flight, which
+// a timeout recorded elsewhere does not end. Bounded by time alone.
+__device__ __forceinline__ bool mbar_drain(uint64_t* bar, uint32_t parity, int where) {
+  return mbar_wait_for<true>(bar, parity, where, kWaitLimitNs);
 }
 
 // 1-D bulk copy global -> shared (TMA engine), completion counted on `bar` in bytes. Both

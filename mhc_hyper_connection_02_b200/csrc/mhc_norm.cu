@@ -434,7 +434,7 @@ struct RowRing {
   // After a wait that gave up in stage st: no copy into this CTA's shared memory may outlive it.
   __device__ __forceinline__ void drain(int st, uint32_t lap, uint32_t j, int ahead) const {
     for (int i = 0; i < ahead && j + i * step < T; ++i) {
-      mbar_wait(&full[st], lap & 1, 131);
+      mbar_drain(&full[st], lap & 1, 131);
       if (++st == S) st = 0, ++lap;
     }
   }

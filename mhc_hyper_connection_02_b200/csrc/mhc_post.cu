@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kPostThreads) post_persistent_kernel(
       if (!ok) {
         for (int i = 0; i < kPostStages; ++i) {
           const int n_i = issued / kPostStages + (i < issued % kPostStages ? 1 : 0);
-          if (n_i > 0) mbar_wait(&full[i], static_cast<uint32_t>((n_i - 1) & 1), 2);
+          if (n_i > 0) mbar_drain(&full[i], static_cast<uint32_t>((n_i - 1) & 1), 2);
         }
       }
     }

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kPpThreads, 1) post_project_kernel(
       }
       if (!ok) {
         for (int64_t i = n - kPpStages; i < n; ++i)
-          if (i >= 0) mbar_wait(&bfull[i & 1], static_cast<uint32_t>(i >> 1) & 1u, 41);
+          if (i >= 0) mbar_drain(&bfull[i & 1], static_cast<uint32_t>(i >> 1) & 1u, 41);
       }
     }
   } else if (warp == 1) {
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kPpThreads, 1) post_project_kernel(
         umma_commit(&accfull[b]);
       }
       umma_commit(done);
-      mbar_wait(done, 0, 45);
+      mbar_drain(done, 0, 45);
     }
   } else {
     // ------------------------------------------------------------------ post-map warps

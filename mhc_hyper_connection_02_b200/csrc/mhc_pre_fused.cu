@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kFsThreads, 1)
       }
       if (!ok) {  // do not leave while copies into shared memory are in flight
         for (int64_t i = it - ST; i < it; ++i)
-          if (i >= 0) mbar_wait(&full[i % ST], static_cast<uint32_t>(i / ST) & 1u, 42);
+          if (i >= 0) mbar_drain(&full[i % ST], static_cast<uint32_t>(i / ST) & 1u, 42);
       }
     }
   } else if (warp == 1) {
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kFsThreads, 1)
       }
       // Every issued MMA has finished before TMEM is released.
       fs_commit(done);
-      mbar_wait(done, 0, 45);
+      mbar_drain(done, 0, 45);
     }
   } else if (warp < kFsCoefWarp0) {
     // ------------------------------------------------------------------ sum of squares + records

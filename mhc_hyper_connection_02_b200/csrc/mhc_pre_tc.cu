@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pre_tc_proj_kernel(
       if (!ok) {  // do not leave while copies into shared memory are in flight
         for (int64_t i = n - ST; i < n; ++i)
           if (i >= 0)
-            mbar_wait(&full[i % ST], static_cast<uint32_t>(i / ST) & 1u, 15);
+            mbar_drain(&full[i % ST], static_cast<uint32_t>(i / ST) & 1u, 15);
       }
     }
   } else if (warp == 1) {
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) pre_tc_proj_kernel(
       }
       // Every issued MMA has finished before TMEM is released.
       umma_commit(done);
-      mbar_wait(done, 0, 14);
+      mbar_drain(done, 0, 14);
     }
   } else {
     // Warps 2..5: TMEM lane quarter q = warp % 4 holds rows 32q..32q+31 of each sub-tile's

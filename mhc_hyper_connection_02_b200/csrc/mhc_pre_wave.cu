@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kWvThreads, 1)
       if (!ok) {  // do not leave while copies into shared memory are in flight
         for (int64_t i = it - kWvStages; i < it; ++i)
           if (i >= 0)
-            mbar_wait(&full[i % kWvStages], static_cast<uint32_t>(i / kWvStages) & 1u, 72);
+            mbar_drain(&full[i % kWvStages], static_cast<uint32_t>(i / kWvStages) & 1u, 72);
       }
     }
   } else if (warp == 1) {
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kWvThreads, 1)
       }
       // Every issued MMA has finished before TMEM is released.
       umma_commit(done);
-      mbar_wait(done, 0, 75);
+      mbar_drain(done, 0, 75);
     }
   } else if (warp < kWvPubWarp) {
     // ------------------------------------------------------------------ sum of squares + records

@@ -43,3 +43,14 @@ def test_selftest_rejects_limits_out_of_range():
         with pytest.raises(mhc.MhcError) as e:
             mhc.selftest_wait_timeout(bad)
         assert e.value.status == mhc.MHC_ERR_INVALID_ARG
+
+
+def test_waits_for_copies_in_flight_outlast_a_recorded_timeout():
+    """The second half of the health check: with MHC_ERR_TIMEOUT recorded, a wait of the kind that
+    kernels end with still lasts until its arrival, 0.1 s later (the word would read
+    MHC_ERR_CUDA)."""
+    torch.cuda.synchronize()
+    assert mhc.device_status() == 0
+    mhc.selftest_wait_timeout(200_000_000)
+    assert mhc.device_status() == mhc.MHC_ERR_TIMEOUT
+    assert mhc.device_status() == 0
