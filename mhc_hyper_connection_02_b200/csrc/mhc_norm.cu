@@ -1123,7 +1123,7 @@ RingPlan ring_plan(int64_t T, int64_t H, int A, int per, int K, int weights, boo
   const int n = static_cast<int>(aligned ? H / VE : (H + 2 * VE - 2) / VE);
   p.G = round32((n + per - 1) / per);
   if (p.G > kRingThreads || H < 2 * VE) return p;
-  p.R = kRingThreads / p.G < 15 ? kRingThreads / p.G : p.G == 32 ? kRingThreads / p.G : 15;
+  p.R = kRingThreads / p.G;  // 16 single warps, or at most 8 groups with a named barrier each
   p.C = aligned ? 1 : VE;
   const size_t stage = static_cast<size_t>(A) * K * (aligned ? n : n + 2) * 16;
   const size_t w = static_cast<size_t>(weights) * n * VE * 4;  // staged weights

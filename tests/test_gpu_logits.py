@@ -563,3 +563,30 @@ def test_maxima_on_either_side_of_the_forms_border(tau, V, reps):
     idx, t = _teacher(T, V, 5, "fp32", 2)
     k = mhc.distill_topk(z, idx, tau * t, temperature=tau)
     _check_distill(z, idx, tau * t, tau, k, "fp32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("V", [77, 3001, 40003])
+def test_gradients_written_into_rows_of_another_phase(dtype, V):
+    """Logits and gradient begin at addresses and lie at distances of their own; what stands beside
+    the gradient's rows stays."""
+    T, K = 7, 6
+    z, y = _logits(T, V, dtype, V), _targets(T, V, 2)
+    idx, t = _teacher(T, V, K, "fp32", 1, ragged=False)
+    a, b = torch.randn(T, device="cuda"), torch.randn(T, device="cuda")
+    _, ent, _, _, st = mhc.token_logprobs(z, y)
+    _, w, _ = mhc.distill_topk(z, idx, t)
+    for first, gap, out_first, out_gap in ((0, 0, 1, 0), (1, 0, 0, 0), (3, 2, 2, 5), (0, 1, 7, 8),
+                                           (5, V, 5, V)):
+        src = torch.zeros(first + T * (V + gap), dtype=z.dtype, device="cuda")
+        zz = torch.as_strided(src, (T, V), (V + gap, 1), first)
+        zz.copy_(z)
+        buf = torch.full((out_first + T * (V + out_gap) + 3,), 7.0, dtype=z.dtype, device="cuda")
+        out = torch.as_strided(buf, (T, V), (V + out_gap, 1), out_first)
+        inside = torch.zeros_like(buf, dtype=torch.bool)
+        torch.as_strided(inside, (T, V), (V + out_gap, 1), out_first).fill_(True)
+        mhc.token_logprobs_backward(zz, y, st, a, d_entropy=b, entropy=ent, d_logits=out)
+        _check_backward(z, y, 1.0, a, b, st, ent, out, dtype)
+        mhc.distill_topk_backward(zz, idx, w, st, a, d_logits=out)
+        _check_distill_backward(z, idx, w, 1.0, a, out, dtype)
+        assert (buf[~inside] == 7).all()

@@ -312,3 +312,52 @@ def test_gradient_of_rows_of_two_neighbouring_values(dtype, low, high, H):
     check(got[0], dx, rounded(dx, ex, dtype), "d_x")
     check(got[1], dg, eg, "d_gamma")
     check(got[2], db, eb, "d_beta")
+
+
+@pytest.mark.parametrize("T,H,dtype,gap", [
+    # rows that are not whole windows: the last staged width and the next, backward and forward
+    (300, 14057, "bf16", 1), (300, 14058, "fp16", 1), (299, 14065, "fp16", 1),
+    (299, 14066, "bf16", 1), (301, 8189, "fp32", 1), (301, 8190, "fp32", 1),
+    (300, 9377, "fp32", 1), (300, 9378, "fp32", 1),
+    # whole windows: the last width whose gradients are held, staged and neither; many tokens beyond
+    (300, 8192, "fp16", 0), (300, 8200, "bf16", 0), (300, 16392, "bf16", 8),
+    (300, 8196, "fp32", 0), (300, 11468, "fp32", 0), (300, 11472, "fp32", 4),
+    (1500, 12288, "fp32", 0), (900, 16384, "fp32", 0)])
+def test_widths_on_either_side_of_the_forms_limits(T, H, dtype, gap):
+    x, dy, gamma, beta = _make(T, H, dtype, "fp32", T + H, gap=gap)
+    got = mhc.layer_norm(x, gamma, beta)
+    _check_forward(x, gamma, beta, got, dtype)
+    back = mhc.layer_norm_backward(dy, x, gamma, got[1], got[2])
+    _check_backward(dy, x, gamma, got[1], got[2], back, dtype)
+
+
+@pytest.mark.parametrize("H", [7168, 3501])
+def test_rows_written_just_before_on_another_stream(H):
+    """Inputs that kernels of the same side stream write just before the call and overwrite just
+    after it, forward and backward, twice over in one graph too."""
+    x, dy, gamma, beta = _make(700, H, "bf16", "fp32", H)
+    y, mean, rstd = mhc.layer_norm(x, gamma, beta)
+    ref = [y, mean, rstd, *mhc.layer_norm_backward(dy, x, gamma, mean, rstd)]
+    a, d = torch.zeros_like(x), torch.zeros_like(dy)
+
+    def both():
+        a.copy_(x)
+        f = mhc.layer_norm(a, gamma, beta)
+        d.copy_(dy)
+        b = mhc.layer_norm_backward(d, a, gamma, f[1], f[2])
+        a.zero_()
+        d.zero_()
+        return [*f, *b]
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = both()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        first, second = both(), both()
+    graph.replay()
+    torch.cuda.synchronize()
+    for g, f, s, w in zip(got, first, second, ref):
+        assert torch.equal(g, w) and torch.equal(f, w) and torch.equal(s, w)
