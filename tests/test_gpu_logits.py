@@ -7,8 +7,8 @@ import torch
 
 import mhc_hyper_connection_02_b200 as mhc
 from oracle import rows
-from rows_util import DTYPES, E2, LN2, U, check, f64, grad_bounds, logprob_bounds, rounded, \
-    row_sum_error
+from rows_util import DTYPES, E2, LN2, U, check, f64, grad_bounds, logprob_bounds, norm_bounds, \
+    norm_bwd_bounds, rounded, row_sum_error
 
 pytestmark = pytest.mark.gpu
 
@@ -590,3 +590,83 @@ def test_gradients_written_into_rows_of_another_phase(dtype, V):
         mhc.distill_topk_backward(zz, idx, w, st, a, d_logits=out)
         _check_distill_backward(z, idx, w, 1.0, a, out, dtype)
         assert (buf[~inside] == 7).all()
+
+
+def test_the_answer_end_of_a_stack_with_its_weights_gradients():
+    """The chain above with every error carried through element by element, so that the bounds of
+    d_x, d_gamma and d_beta lie far below their values: a lost or a wrong part of them shows."""
+    T, H, V, K = 24, 512, 4001, 12
+    g = torch.Generator().manual_seed(1)
+    R = torch.randn((T, 4, H), generator=g).to(torch.bfloat16).cuda()
+    gamma = (1 + 0.1 * torch.randn(H, generator=g)).cuda()
+    beta = (0.1 * torch.randn(H, generator=g)).cuda()
+    W = (torch.randn((H, V), generator=g) / H ** 0.5).cuda()
+    y = _targets(T, V, 6)
+    idx, t = _teacher(T, V, K, "fp32", 2)
+    x = mhc.head_mean(R).float()
+    n, mean, rstd = mhc.layer_norm(x, gamma, beta)
+    z = n @ W
+    lp, ent, _, _, st = mhc.token_logprobs(z, y)
+    loss, w, st2 = mhc.distill_topk(z, idx, t, temperature=2.0)
+    a = torch.full((T,), -1.0 / T, device="cuda")
+    dz = mhc.token_logprobs_backward(z, y, st, a, d_entropy=0.01 * a, entropy=ent)
+    dz += mhc.distill_topk_backward(z, idx, w, st2, -a, temperature=2.0)
+    got = mhc.layer_norm_backward(dz @ W.t(), x, gamma, mean, rstd)
+    ref, tol = _answer_end(f64(x), f64(gamma), f64(beta), f64(W), y.cpu().numpy(),
+                           idx.cpu().numpy(), f64(t), f64(a))
+    for v, r, e, what in zip(got, ref, tol, ("d_x", "d_gamma", "d_beta")):
+        assert np.max(e) < np.max(np.abs(r)) / 50, what
+        check(v, r, e, what)
+
+
+def _answer_end(x, gamma, beta, W, y, idx, t, a):
+    """(d_x, d_gamma, d_beta) of the chain in fp64, and bounds of their errors in fp32. To first
+    order: an error ez of each logit moves ln p and the entropy's term by at most twice its largest,
+    and p by that times p."""
+    H, V = W.shape
+    n, mean, rstd = rows.layer_norm(x, gamma, beta)
+    ey, em, er = norm_bounds(x, gamma, beta, n, mean, rstd, 1e-6)
+    z = n @ W
+    # the product: sums of H terms, and the error of what it takes (rounded once)
+    ez = (H + 8) * U * (np.abs(n) @ np.abs(W)) + rounded(n, ey, "fp32") @ np.abs(W)
+    shift = 2 * ez.max(1)
+    r, r2 = rows.token_logprobs(z, y, 1.0), rows.token_logprobs(z, None, 2.0)
+    h = 0.01 * a
+    dz = rows.token_logprobs_backward(z, y, 1.0, a, h)
+    w = rows.distill_topk(z, idx, t, 2.0)[1]
+    dz2 = rows.distill_topk_backward(z, idx, w, -a, 2.0)
+    p, p2 = np.exp(r["lp"]), np.exp(r2["lp"])
+    size = np.abs(r["lp"]) + r["entropy"][:, None]
+    ab = np.abs(a)[:, None]
+    s = shift[:, None]
+    e_ent = logprob_bounds(r, z, 1.0)[1][:, None]
+    ed = (grad_bounds(r["lp"], r["entropy"], 1.0, a, h,
+                      row_sum_error(z, r["m"], 1.0)[:, None] + U)
+          + ab * p * s + np.abs(h)[:, None] * p * (s * (size + 2) + e_ent)
+          + grad_bounds(r2["lp"], r2["entropy"], 2.0, a, 0 * a,
+                        row_sum_error(z, r2["m"], 2.0)[:, None] + U) + ab / 2 * p2 * s / 2)
+    # the target's and the entries' own terms: weights within 64 U, sums of at most K + 8 terms
+    own = np.zeros_like(z)
+    rows_ = np.arange(len(a))
+    own[rows_[y >= 0], y[y >= 0]] = 8 * U
+    for k in range(idx.shape[1]):
+        used = idx[:, k] >= 0
+        np.add.at(own, (rows_[used], idx[used, k]), (64 + 2 * idx.shape[1]) * U * w[used, k])
+    ed = ed + ab * own + 2 * U * (np.abs(dz) + np.abs(dz2))
+    dz = dz + dz2
+    dn = dz @ W.T
+    edn = ed @ np.abs(W).T + (V + 8) * U * (np.abs(dz) @ np.abs(W).T)
+    ref = rows.layer_norm_backward(dn, x, gamma, mean, rstd)
+    ex, eg, eb = norm_bwd_bounds(dn, x, gamma, mean, rstd)
+    # what the backward pass is given: d_y within edn, mean within em, rstd within er
+    rs, er = rstd[:, None], er[:, None]
+    xh = np.abs(x - mean[:, None]) * rs
+    exh = rs * em[:, None] + xh * er / rs
+    q, eq = np.abs(dn * gamma), edn * np.abs(gamma)
+    c1, c2 = q.mean(1, keepdims=True), (q * xh).mean(1, keepdims=True)
+    ec2 = (eq * xh + q * exh).mean(1, keepdims=True)
+    ex = ex + rs * (eq + eq.mean(1, keepdims=True) + exh * c2 + xh * ec2) + er * (q + c1 + xh * c2)
+    eg = eg + (edn * xh + np.abs(dn) * exh).sum(0)
+    eb = eb + edn.sum(0)
+    # second-order terms, and fp32's rounding of d_x
+    return ref, (1.01 * ex + 2 * U * np.abs(ref[0]), 1.01 * eg, 1.01 * eb)
