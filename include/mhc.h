@@ -210,8 +210,9 @@ MHC_API int mhc_device_status(mhc_stream_t stream);
  * and returns; no copy is in flight, so the context stays usable. With the timeout recorded it also
  * makes a wait of the kind that kernels end with (for their own copies in flight), which has to last
  * until its arrival half a limit later. A following mhc_device_status() returns MHC_ERR_TIMEOUT
- * (and clears the word), or MHC_ERR_CUDA where that second wait gave up. Errors: MHC_ERR_INVALID_ARG (limit out of range),
- * MHC_ERR_UNSUPPORTED (current device not sm_100), MHC_ERR_CUDA (launch failed). */
+ * (and clears the word), or MHC_ERR_CUDA where that second wait gave up. Errors:
+ * MHC_ERR_INVALID_ARG (limit out of range), MHC_ERR_UNSUPPORTED (current device not sm_100),
+ * MHC_ERR_CUDA (launch failed). */
 MHC_API int mhc_selftest_wait_timeout(int64_t limit_ns, mhc_stream_t stream);
 
 /*
@@ -409,7 +410,11 @@ enum mhc_dtype {
  *   d_gamma and d_beta are set to zero (the one thing written); workspace of
  *   mhc_layer_norm_backward_workspace_bytes(T, H) bytes, 256-byte aligned.
  * Errors: MHC_ERR_INVALID_ARG, MHC_ERR_WORKSPACE_TOO_SMALL, MHC_ERR_ALIAS (an output overlapping an
- * input or another output, y == x apart).
+ * input or another output, y == x apart). The forms that stage rows in shared memory (the backward
+ * pass, and the forward pass of many rows that are not whole 16-byte windows) wait for their copies,
+ * with a limit: where a wait gives up, or finds the status word still set by an earlier call,
+ * outputs stay partly unwritten although the call returned MHC_OK, and mhc_device_status() says
+ * MHC_ERR_TIMEOUT.
  */
 MHC_API int mhc_layer_norm(const void* x, int64_t x_stride, int dtype, const void* gamma,
                            const void* beta, int w_dtype, void* y, float* mean, float* rstd,
@@ -446,9 +451,10 @@ enum {
  * mhc_token_logprobs_backward  d_logits = (d_logprob (1[v = target] - p_v)
  *                                          - d_entropy p_v (ln p_v + entropy)) / temperature
  *   d_logprob, d_entropy [T] fp32, one of them may be NULL (zero), finite in fp32 when divided by
- *   temperature; entropy as the forward pass gave it (with d_entropy); targets with d_logprob. d_logits [T][V] of dtype, rows d_row_stride apart,
- *   rounded once; may be exactly logits (same stride). Rows whose upstream gradients are zero get
- *   zeros, whatever their logits. The top alternatives have no gradient.
+ *   temperature; entropy as the forward pass gave it (with d_entropy); targets with d_logprob.
+ *   d_logits [T][V] of dtype, rows d_row_stride apart, rounded once; may be exactly logits (same
+ *   stride). Rows whose upstream gradients are zero get zeros, whatever their logits. The top
+ *   alternatives have no gradient.
  * temperature: finite and > 0 (and so are 1 / temperature and log2(e) / temperature).
  * Errors: MHC_ERR_INVALID_ARG; MHC_ERR_ALIAS (an output overlapping an input, in place apart).
  */

@@ -707,8 +707,8 @@ def layer_norm_backward(d_y, x, gamma, mean, rstd, *, d_x=None, workspace=None, 
 
 def _grad_rows(logits, T, V, stride):
     """An uninitialised gradient of the logits' type. Where the logits' rows are padded by less than
-    an eighth (a vocabulary rounded up for the product that made them), the gradient's are too: the
-    next product wants its rows aligned as well."""
+    an eighth (a vocabulary rounded up for the product that made them; more is a slice of something
+    else), the gradient's are too: the next product wants its rows aligned as well."""
     if V < stride <= V + V // 8:
         return logits.new_empty((T, stride))[:, :V]
     return _dense_like(logits)

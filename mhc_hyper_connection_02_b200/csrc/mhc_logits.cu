@@ -32,6 +32,10 @@ constexpr int kLgTopMax = MHC_TOP_MAX;
 constexpr float kDCut = -200.0f;  // 2^-200 is zero in fp32: cutting d there keeps 0 * d finite
 constexpr float kLn2 = 0.693147180559945309f;
 
+// The hardware's base-2 exponential: relative error up to 2^-22, four times that of a rounded one, in
+// every sum, weight and gradient here (fp32 outputs are off by about 1.5e-7 where plain fp32
+// arithmetic's are by 5e-8). A more exact one takes several instructions more an element, in passes
+// that issue slots bound next to memory. Results below 2^-126 are 0.
 __device__ __forceinline__ float ex2(float d) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d));
@@ -108,9 +112,9 @@ struct ThreadBest {
 //
 // ex2 runs at 16 a clock and SM: a warp's takes 8 of the 11 cycles that HBM's rate allows an element
 // of bf16. The rest is therefore done on packed values (maximum, cut) and on pairs of fp32.
-// T=8192, V=131072, bf16: 303 us, with entropy 314 us (7.1 and 6.8 TB/s) in a burst, without packed
-// values and pairs 352 and 406 us; under seconds of load the SMs' clock falls to 1.56 GHz at the power
-// cap, and ex2 brings them to 357 and 383 us.
+// T=8192, V=131072, bf16: 310 us, with entropy 319 us (6.9 and 6.7 TB/s) in a burst, without packed
+// values and pairs 352 and 406 us. Under seconds of load they take 359 and 387 us, at the power cap
+// and 1.55 GHz: ex2 by itself would take 290 us there, so it is not the bound alone.
 template <int DT, int NT, bool kEnt>
 __device__ __forceinline__ RowSums thread_sums(const typename Elem<DT>::raw* row, const RowPart& p,
                                                float c, ThreadBest& best) {
@@ -740,7 +744,7 @@ __device__ __forceinline__ void grad_window(uint4 w, const GradRow& g, float (&x
 constexpr int kLgRounds = 2;
 // CTAs that an SM has to hold: 1536 threads, at 40 registers. The passes wait for memory, and with
 // 1024 threads of 64 registers the distillation's took 376 us, with 1280 339 us, with these 331 us
-// (T=4096, V=131072, bf16).
+// (T=4096, V=131072, bf16), although 24 to 60 bytes a thread of its entry then go to local memory.
 constexpr int grad_ctas(int threads) { return threads > 32 ? 1536 / threads : 1; }
 template <int DT, int NT>
 struct GradChunk {
@@ -792,7 +796,7 @@ struct GradChunk {
 };
 
 // Gradient of log probability and entropy, a chunk per CTA. The first windows are read before
-// anything else. Bound by HBM: T=8192, V=131072 bf16 620 us, 6.9 TB/s (read and written once).
+// anything else. Bound by HBM: T=8192, V=131072 bf16 625 us, 6.9 TB/s (read and written once).
 template <int DT, int NT, bool kEnt>
 __global__ void __launch_bounds__(NT, grad_ctas(NT)) logprob_grad_kernel(const LogitGradArgs a) {
   constexpr int VE = Elem<DT>::kVec;
@@ -1010,7 +1014,11 @@ int by_threads(int threads, F&& f) {
 
 // Launches a kernel of a cluster per row, in two parts where few rows are left over after full rounds
 // of `ctas` CTAs an SM and a row is long (from 128 KB): 66 -> 61 us for T=1500, V=100003 bf16 with 5
-// alternatives, but 51 -> 54 us for T=3000, V=30000.
+// alternatives, but 51 -> 54 us for T=3000, V=30000. Few are up to a quarter of a round: in one launch
+// and in two, for 1/32, 1/8, 1/4, 3/8 and 1/2 of a round left over after one round of V=131072 bf16
+// 59 and 47, 61 and 51, 64 and 59, 68 and 68, 72 and 72 us; after three rounds 125 and 119, 127 and
+// 121, 131 and 127, 133 and 135, 137 and 137 us; after one round of V=66001 35 and 31, 37 and 33, 41
+// and 37, 41 and 41, 43 and 43 us.
 template <typename A>
 int launch_split(void (*kernel)(A), int64_t T, int vec, int threads, int ctas, size_t smem,
                  cudaStream_t s, A a) {

@@ -670,11 +670,11 @@ __global__ void __launch_bounds__(kRingThreads) norm_ring_kernel(const NormArgs 
 // twice, and exchanges the sums of K tokens at once. Each thread keeps its columns' gradient sums in
 // registers over all its tokens: 16 columns at 512 threads an SM, which is what they and two held
 // rows leave room for; with 8 columns at 1024 threads each warp's exchange costs as much for half the
-// work (T=8192, H=7168 bf16: 112 us instead of 67 us). All waits are bounded, and a group leaves its
-// loop together.
+// work (T=8192, H=7168 bf16: 110 us, where this form took 87 us before its later steps). All waits
+// are bounded, and a group leaves its loop together.
 //
-// 67 us are 5.3 TB/s, 80 % of the copy rate; H=3501 56 us. The copies alone take 40 us: what bounds
-// the pass is the latency of a warp's instructions (14 warps an SM, 45 % of issue slots used).
+// Now 68.5 us, 5.1 TB/s and 78 % of the copy rate; H=3501 57 us. The copies alone take 40 us: what
+// bounds the pass is the latency of a warp's instructions (14 warps an SM, 46 % of issue slots used).
 template <int DT, int WT, int N, int K, bool kHold, bool kAligned>
 __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormBwdArgs a, int G, int R,
                                                             int S, int C) {
