@@ -670,3 +670,28 @@ def _answer_end(x, gamma, beta, W, y, idx, t, a):
     eb = eb + edn.sum(0)
     # second-order terms, and fp32's rounding of d_x
     return ref, (1.01 * ex + 2 * U * np.abs(ref[0]), 1.01 * eg, 1.01 * eb)
+
+
+def test_rows_left_over_after_full_rounds_in_a_graph():
+    """The two launches of such a call captured between writers of their logits, twice over, and
+    replayed with other logits."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    T, V = sms * 6 + 9, 66001
+    src, y = _logits(T, V, "bf16", 1), _targets(T, V, 2)
+    other = torch.randn((T, V), device="cuda").to(torch.bfloat16)
+    ref = [mhc.token_logprobs(v, y) for v in (src, other)]
+    z = torch.zeros_like(src)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = []
+        for _ in range(2):
+            z.copy_(src)
+            got.append(mhc.token_logprobs(z, y))
+            z.zero_()
+    for want in ref:
+        graph.replay()
+        torch.cuda.synchronize()
+        for one in got:
+            for k in (0, 1, 4):
+                assert torch.equal(one[k], want[k])
+        src.copy_(other)
