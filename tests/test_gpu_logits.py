@@ -7,8 +7,9 @@ import torch
 
 import mhc_hyper_connection_02_b200 as mhc
 from oracle import rows
-from rows_util import DTYPES, E2, LN2, U, check, f64, grad_bounds, logprob_bounds, norm_bounds, \
-    norm_bwd_bounds, rounded, row_sum_error
+from rows_util import DTYPES, E2, LN2, U, check, f64, grad_bounds, logprob_bounds, rounded, \
+    row_sum_error
+from rows_util import norm_bounds, norm_bwd_bounds
 
 pytestmark = pytest.mark.gpu
 
